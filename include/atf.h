@@ -300,9 +300,128 @@ atf_status atf_fasa_decode(const void* q_rot, const void* k_chunked, const void*
                            void* workspace, size_t workspace_bytes, void* stream);
 size_t atf_fasa_workspace_bytes(int batch, int heads, long long n_cache, int budget, int d);
 
+/* Norms of queries and keys for each head, with the position rotation in the
+ * same pass: what sits between a fused projection and the attention.
+ *   y = x / sqrt(mean(x^2) + eps) * weight  over the d elements of a head (a NULL
+ *       weight: y = x), then pair i of y is turned by pos[axis of i] * theta^(-2i/d).
+ * Computed in fp32 (angles reduced in fp64) and rounded once.  The outputs hold
+ * pair i in dims (2i, 2i+1): what atf_prefill_ex reads with rotated = 1. */
+typedef struct {
+  const void *q, *k;       /* token t, head h at element t * stride + h * d of [tokens][...]; slices of one
+                              fused projection are fine */
+  long long q_stride, k_stride; /* elements from a token to the next: >= heads * d, rows 16-byte aligned */
+  void *q_out, *k_out;     /* [tokens][heads][d] and [tokens][kv_heads][d], contiguous; must not overlap
+                              each other or an input */
+  const void *q_weight, *k_weight; /* [d] of the same dtype, in the order of the input's dims, or NULL */
+  const long long* pos;    /* DEVICE [n_axes][tokens] positions, |pos| < 2^31 */
+  const unsigned char* pair_axis; /* HOST, d/2 entries < n_axes: the position axis of each pair (time, row,
+                              column of image or video tokens); NULL: axis 0 */
+  int tokens, heads, kv_heads, d; /* heads or kv_heads 0: no queries / no keys (their pointers are ignored) */
+  int n_axes;              /* 1 .. 4 */
+  int pairing, dtype;      /* atf_pairing of the inputs; atf_dtype of all tensors */
+  double theta;
+  float eps;               /* >= 0 */
+} atf_qk_norm_rope_args;
+atf_status atf_qk_norm_rope(const atf_qk_norm_rope_args* args, void* stream);
+
+/* Paged key-value cache, shared by the three calls below.  A pool of num_pages
+ * pages of page_size (16, 32, 64 or 128) slots:
+ *   k_pages: [num_pages][kv_heads][d/16][page_size][16] bf16, rotated keys, pairs
+ *            interleaved, 8-pair chunks (the order of atf_decode's cache, page by page);
+ *   v_pages: [num_pages][kv_heads][page_size][d] bf16;
+ *   bounds:  [num_pages][kv_heads][2][d] bf16: minimum and maximum of the page's keys
+ *            in each dim (interleaved order), read by atf_page_select.
+ * Token n of sequence b is in slot n % page_size of page
+ * page_table[b * max_pages + n / page_size].  Tables and lengths are int32 arrays in
+ * DEVICE memory and are read when the kernels run, so that a captured graph follows a
+ * growing sequence.  Their contents cannot be checked by the call: a page index outside
+ * [0, num_pages), a length above max_pages * page_size, row offsets outside the input or
+ * a selected page behind the last are skipped by the kernels (never read or written
+ * through) and reported by the next atf_check as ATF_ERR_INVALID_ARG; what the call
+ * computes for those sequences is unspecified.  Pages may be shared between sequences
+ * for reading; two tokens appended to one slot in one call, or two sequences that append
+ * into one page, leave it unspecified. */
+
+/* Appends new tokens of a batch to a paged cache: keys normed and rotated as by
+ * atf_qk_norm_rope, values as they are, the bounds of the touched pages brought up to
+ * date, and the tokens' queries, normed and rotated, to q_out. */
+typedef struct {
+  const void *q, *k, *v;   /* bf16 rows, as in atf_qk_norm_rope; q NULL: no queries */
+  long long q_stride, k_stride, v_stride;
+  void* q_out;             /* [tokens][heads][d]; rows of no sequence are left as they are; must not overlap
+                              an input */
+  void *k_pages, *v_pages;
+  void* bounds;            /* NULL: not kept.  A page whose slot 0 is written starts its bounds anew, any
+                              other adds to them; keys are expected to be finite */
+  const void *q_weight, *k_weight; /* [d] bf16 or NULL */
+  const int* page_table;   /* DEVICE [batch][max_pages] */
+  const int* start;        /* DEVICE [batch]: tokens that the sequence already holds, the slot of its first
+                              new token; negative: a padding row, nothing is written for it */
+  const int* cu;           /* DEVICE [batch + 1]: sequence b's new tokens are rows cu[b] .. cu[b+1] - 1 (rows
+                              behind cu[batch] are padding); NULL: one token each, tokens == batch */
+  const long long* pos;    /* DEVICE [n_axes][tokens]; NULL (n_axes 1): a token's position is its slot number in
+                              the sequence.  Distances in atf_paged_decode are those of the slots */
+  const unsigned char* pair_axis; /* HOST, as in atf_qk_norm_rope */
+  long long num_pages;
+  int tokens, batch, heads, kv_heads, d, page_size, max_pages;
+  int n_axes, pairing;
+  double theta;
+  float eps;
+} atf_paged_append_args;
+atf_status atf_paged_append(const atf_paged_append_args* args, void* stream);
+
+/* Decode over a paged cache: one query per sequence, at position kv_len[b] - 1, with the
+ * windows of the method, over every key of the sequence or over the pages of a list. */
+typedef struct {
+  const void* q;           /* bf16 [batch] rows of [heads][d], ALREADY rotated (atf_paged_append's q_out) */
+  long long q_stride;      /* elements from a sequence to the next: >= heads * d, rows 16-byte aligned */
+  const void *k_pages, *v_pages;
+  const int* page_table;   /* DEVICE [batch][max_pages] */
+  const int* kv_len;       /* DEVICE [batch]: live keys, the query's own included; 0 or less: the output is 0 */
+  const int* selected;     /* DEVICE [batch][kv_heads][n_select] pages of the sequence (as atf_page_select writes),
+                              the first min(n_select, pages of the sequence) entries are read, -1 skipped; a
+                              page listed twice counts twice.  NULL: every page */
+  void* out;               /* bf16 [batch][heads][d] */
+  float* lse;              /* [batch][heads] natural logarithm of the softmax sum (-inf without a key), or NULL */
+  long long num_pages;
+  int batch, heads, kv_heads, d, page_size, max_pages, n_select;
+  double theta, alpha;
+  void* workspace;         /* DEVICE, atf_paged_decode_workspace_bytes(...); need not be cleared, and must not be
+                              in use by another call that may run at the same time */
+  size_t workspace_bytes;
+} atf_paged_decode_args;
+atf_status atf_paged_decode(const atf_paged_decode_args* args, void* stream);
+size_t atf_paged_decode_workspace_bytes(int batch, int heads, int kv_heads, int d);
+
+/* Chooses, for each sequence and kv head, the n_select pages that its query attends to:
+ * the first n_first and the last n_last pages of the sequence and then those of the highest
+ *   max over the kv head's query heads of
+ *   sum over pairs i with (kv_len - 1 - last key of the page) <= W_i, and their two dims e,
+ *   of max(q_e * minimum_e, q_e * maximum_e)
+ * (an upper bound of the logits of the page's keys where all pairs are in reach; 64-bit sums),
+ * equal ones by lower index. */
+typedef struct {
+  const void* q;           /* as in atf_paged_decode */
+  long long q_stride;
+  const void* bounds;
+  const int* page_table;   /* DEVICE [batch][max_pages] */
+  const int* kv_len;       /* DEVICE [batch] */
+  int* selected;           /* DEVICE [batch][kv_heads][n_select]: ascending page numbers of the sequence, -1 past
+                              min(n_select, its pages) */
+  long long num_pages;
+  int batch, heads, kv_heads, d, page_size, max_pages;
+  int n_select, n_first, n_last; /* n_first + n_last <= n_select */
+  double theta, alpha;
+  void* workspace;         /* DEVICE, atf_page_select_workspace_bytes(...), as in atf_paged_decode */
+  size_t workspace_bytes;
+} atf_page_select_args;
+atf_status atf_page_select(const atf_page_select_args* args, void* stream);
+size_t atf_page_select_workspace_bytes(int batch, int kv_heads, int max_pages);
+
 /* Synchronises `stream` and reports ATF_ERR_TIMEOUT if any kernel of this
  * library on the current device gave up a bounded wait since the last
- * atf_check (the device error word is cleared), ATF_ERR_CUDA on a CUDA error. */
+ * atf_check (the device error word is cleared), ATF_ERR_INVALID_ARG if one skipped
+ * bad data in a device array (page tables and lengths), ATF_ERR_CUDA on a CUDA error. */
 atf_status atf_check(void* stream);
 
 /* Failure-detection self test: launches one CTA that waits on a barrier that

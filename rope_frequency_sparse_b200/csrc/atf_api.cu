@@ -179,6 +179,28 @@ atf_status atf::report_error(atf_status st, const char* fmt, ...) {
   return st;
 }
 
+atf_status atf::check_method(int d, double theta, double alpha) { return check_params(d, theta, alpha); }
+
+void atf::method_windows(int d, double theta, double alpha, Windows* out, double* omega) {
+  kernel_windows(d, theta, alpha, out, omega);
+}
+
+atf_status atf::tensor_map_4d(CUtensorMap* map, const void* base, const unsigned long long dims[4],
+                              const unsigned long long strides[3], const unsigned int box[4],
+                              CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(ATF_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  cuuint64_t cd[4], cs[3];
+  cuuint32_t cb[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) cd[i] = dims[i], cb[i] = box[i];
+  for (int i = 0; i < 3; ++i) cs[i] = strides[i];
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), cd, cs, cb, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATF_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return ATF_OK;
+}
+
 extern "C" {
 
 const char* atf_last_error(void) { return g_last_error.c_str(); }
@@ -529,6 +551,13 @@ atf_status atf_check(void* stream) {
   if (code) {
     const unsigned int zero = 0;
     cudaMemcpyToSymbol(g_atf_device_error, &zero, sizeof zero);
+    if (code & kErrBadData) {
+      const char* what = code == kErrBadPage     ? "a page index outside the pool"
+                         : code == kErrBadLength ? "a sequence longer than its page table"
+                         : code == kErrBadRows   ? "row offsets outside the input rows"
+                                                 : "a selected page behind its sequence's last";
+      return fail(ATF_ERR_INVALID_ARG, "a kernel skipped bad data in a device array: %s", what);
+    }
     return fail(ATF_ERR_TIMEOUT, "a kernel gave up a bounded wait (code 0x%x)", code);
   }
   return ATF_OK;

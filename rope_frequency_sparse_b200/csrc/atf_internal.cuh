@@ -72,7 +72,82 @@ struct AppendParams {
   double omega[kMaxPairs];
 };
 
+// Rotation angles of up to four position axes: pair i of a token turns by
+// pos[axis of i] * theta^(-2i/d), held in turns.
+constexpr int kMaxAxes = 4;
+struct RotaryTable {
+  double turns[kMaxPairs];          // theta^(-2i/d) / (2 pi)
+  unsigned char axis[kMaxPairs];    // < kMaxAxes
+  int n_axes;
+};
+
+struct NormRopeParams {
+  const void *q, *k;                // token t, head h at element t * stride + h * d
+  long long q_stride, k_stride;
+  void *q_out, *k_out;              // contiguous [tokens][heads][d], pairs interleaved
+  const void *q_weight, *k_weight;  // [d] in the element type, nullable: no norm
+  const long long* pos;             // [n_axes][tokens]
+  int tokens, hq, hkv, d, pairing, fp32;
+  float eps;
+  RotaryTable rot;
+};
+
+struct PagedAppendParams {
+  const void *q, *k, *v;            // q nullable; token t, head h at element t * stride + h * d, bf16
+  long long q_stride, k_stride, v_stride;
+  void* q_out;                      // [tokens][hq][d]
+  void *k_pages, *v_pages, *bounds; // bounds nullable
+  const void *q_weight, *k_weight;
+  const int *page_table, *start, *cu;  // cu nullable: one token per sequence
+  const long long* pos;             // nullable: the slot
+  int tokens, batch, hq, hkv, d, pairing, page_log2, max_pages, num_pages;
+  float eps;
+  unsigned int* err;
+  RotaryTable rot;
+};
+
+struct PagedDecodeParams {
+  const void* q;          // rotated queries, sequence b at element b * q_stride
+  long long q_stride;
+  const int *page_table, *kv_len, *selected;  // selected nullable: [batch][hkv][n_sel] logical pages
+  void* out;              // [batch][hq][d] bf16
+  float* lse;             // nullable [batch][hq]
+  float* partials;        // [kPagedCtas][2][8][d + 2]
+  int4* meta;             // [kPagedCtas]: split sequence, kv head, last CTA of the sequences begun by each CTA
+  int batch, hq, hkv, d, page_log2, max_pages, num_pages, n_sel;
+  unsigned int* err;
+  Windows win;
+};
+
+struct PageSelectParams {
+  const void* q;
+  long long q_stride;
+  const void* bounds;     // [num_pages][hkv][2][d] bf16
+  const int *page_table, *kv_len;
+  unsigned long long* keys;  // [batch][hkv][max_pages] scores in sortable form
+  int* selected;          // [batch][hkv][n_sel]
+  int batch, hq, hkv, d, page_log2, max_pages, num_pages, n_sel, n_first, n_last;
+  unsigned int* err;
+  Windows win;
+};
+
+// CTAs of a paged decode: one per SM of a B200.
+constexpr int kPagedCtas = 148;
+
+// Codes of the device error word for bad data in device arrays (the entry is
+// skipped); bounded waits that expired record smaller codes.
+constexpr unsigned int kErrBadData = 0x10000u;
+constexpr unsigned int kErrBadPage = kErrBadData | 1;    // page index outside the pool
+constexpr unsigned int kErrBadLength = kErrBadData | 2;  // more keys than the page table holds
+constexpr unsigned int kErrBadRows = kErrBadData | 3;    // row offsets outside the input
+constexpr unsigned int kErrBadSelect = kErrBadData | 4;  // selected page behind the sequence
+
 // Launchers (return cudaGetLastError() of the launch).
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                cudaStream_t s);
+cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillParams& p, cudaStream_t s);
@@ -88,6 +163,17 @@ unsigned int* device_error_word();
 
 // Records a printf-style message as this thread's atf_last_error() and returns st.
 atf_status report_error(atf_status st, const char* fmt, ...);
+
+// Checks d, theta and alpha; records a message and returns its status.
+atf_status check_method(int d, double theta, double alpha);
+
+// Windows of the pairs in the kernels' integer domain; omega (kMaxPairs entries) nullable.
+void method_windows(int d, double theta, double alpha, Windows* out, double* omega);
+
+// Tiled tensor map of a 4-D bf16 tensor (dims innermost first, strides of dims
+// 1..3 in bytes); elements outside read as zero.
+atf_status tensor_map_4d(CUtensorMap* map, const void* base, const unsigned long long dims[4],
+                         const unsigned long long strides[3], const unsigned int box[4], CUtensorMapSwizzle swizzle);
 
 // Number of key-range splits per (sequence, kv head) for a decode launch.
 int decode_num_splits(long long max_kv_len, int batch, int hkv);
