@@ -133,6 +133,7 @@ struct PageSelectParams {
 
 // CTAs of a paged decode: one per SM of a B200.
 constexpr int kPagedCtas = 148;
+constexpr int kPagedTileKeys = 64;  // keys of a tile of its work
 
 // Codes of the device error word for bad data in device arrays (the entry is
 // skipped); bounded waits that expired record smaller codes.

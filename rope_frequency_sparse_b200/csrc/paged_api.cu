@@ -259,17 +259,19 @@ atf_status atf_paged_decode(const atf_paged_decode_args* a, void* stream) {
   p.num_pages = static_cast<int>(a->num_pages);
   p.n_sel = a->selected ? a->n_select : 0;
   method_windows(a->d, a->theta, a->alpha, &p.win, nullptr);
-  // keys (16 elements, slot, chunk, page and head), 32-byte swizzle: a box is a
-  // page's chunks; values (64 elements, slot, half of the row, page and head),
-  // 128-byte swizzle: a box is a page's rows, half by half
+  // keys (64 elements: a chunk of four slots, group of four slots, chunk, page and
+  // head): a box is the chunks of up to a tile's slots; values (64 elements, slot,
+  // half of the row, page and head): a box is as many rows, half by half; both with
+  // the 128-byte swizzle
   const unsigned long long d = a->d, ps = a->page_size;
   const unsigned long long rows = static_cast<unsigned long long>(a->num_pages) * a->kv_heads;
-  const unsigned long long kd[4] = {16, ps, d / 16, rows}, ks[3] = {32, ps * 32, ps * d * 2};
-  const unsigned int kb[4] = {16, static_cast<unsigned>(ps), static_cast<unsigned>(d / 16), 1};
+  const unsigned long long kd[4] = {64, ps / 4, d / 16, rows}, ks[3] = {128, ps * 32, ps * d * 2};
+  const unsigned box = a->page_size < kPagedTileKeys ? a->page_size : kPagedTileKeys;
+  const unsigned int kb[4] = {64, box / 4, static_cast<unsigned>(d / 16), 1};
   const unsigned long long vd[4] = {64, ps, d / 64, rows}, vs[3] = {d * 2, 128, ps * d * 2};
-  const unsigned int vb[4] = {64, static_cast<unsigned>(ps), static_cast<unsigned>(d / 64), 1};
+  const unsigned int vb[4] = {64, box, static_cast<unsigned>(d / 64), 1};
   CUtensorMap tk, tv;
-  if (atf_status st = tensor_map_4d(&tk, a->k_pages, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_32B)) return st;
+  if (atf_status st = tensor_map_4d(&tk, a->k_pages, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
   if (atf_status st = tensor_map_4d(&tv, a->v_pages, vd, vs, vb, CU_TENSOR_MAP_SWIZZLE_128B)) return st;
   cudaError_t e = launch_paged_decode(p, tk, tv, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATF_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));

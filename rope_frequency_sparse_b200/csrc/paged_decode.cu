@@ -11,7 +11,7 @@
 // chunk is filled with zeros without being read.
 //
 // Lengths and page tables stay on the device, so a captured call follows growing
-// sequences.  The work of the batch is one list of 128-key tiles, ordered by
+// sequences.  The work of the batch is one list of 64-key tiles, ordered by
 // (sequence, kv head, tile) and weighted by the bytes each tile reads; each of
 // 148 CTAs (one per SM) takes an equal piece of it.  A CTA finds its piece from
 // the lengths alone: closed-form tile weights, a block-wide prefix sum over the
@@ -20,12 +20,15 @@
 // the last of its list), each written as a partial (sum, max, row sum), and a
 // second kernel joins them.
 //
-// Inside a CTA a producer warp walks the list, looks pages up one tile ahead and
-// fills a ring of tiles with TMA; four consumer warps take 32 keys of each tile.
+// Inside a CTA four producer warps walk the list and fill a ring of tiles with TMA,
+// every fourth tile each; a lane looks up the page of one box of 32, a group of
+// boxes ahead (one producer warp that looked pages up tile by tile held the ring
+// empty: 1090 us against 941 for four sequences of 1048576 keys, 28 query and 4 kv
+// heads).  Two groups of four consumer warps take the tiles in turn, 16 keys a warp.
 // Keys are the M rows and query heads (up to 8) the N columns of the warp-level
 // MMAs, S^T = K~ Q~^T and O^T += V^T P^T, so no row of them is padding; P^T
 // goes from accumulators to operand by a register transpose (movmatrix).  P is
-// rounded to bf16 for the product with V (relative 2^-9 a weight, as the prefill
+// rounded to bf16 for the product with V (relative 2^-8 a weight, as the prefill
 // and decode do); its sums, the maxima and O stay fp32.
 #include <cuda_bf16.h>
 
@@ -38,10 +41,13 @@ namespace atf {
 
 namespace {
 
-constexpr int kPdConsumers = 4;
-constexpr int kPdThreads = (kPdConsumers + 1) * 32;
-constexpr int kTileKeys = 128;
-constexpr int kMaxTilePages = 8;  // pages of 16
+constexpr int kPdConsumers = 8;  // two groups of four warps, 16 keys of a tile apiece
+constexpr int kPdProducers = 4;  // warps that fill the ring, every fourth tile each
+constexpr int kPdThreads = (kPdConsumers + kPdProducers) * 32;
+constexpr int kTileKeys = kPagedTileKeys;
+constexpr int kTileLog2 = 6;
+static_assert(1 << kTileLog2 == kTileKeys, "tile");
+constexpr int kMaxTilePages = 4;  // boxes of 16 keys
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -50,20 +56,19 @@ struct PdCfg {
   static constexpr int NC = D / 16;
   static constexpr int HALF = kTileKeys * D * 2;  // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int NSTG = D == 128 ? 3 : 6;
+  static constexpr int NSTG = D == 128 ? 5 : 8;
   static constexpr int Q = 8 * D * 2;
   static constexpr int OROW = D + 4;              // padded so that a warp's stores spread over the banks
   static constexpr int MERGE = kPdConsumers * 8 * OROW * 4;
 };
 
 struct StageInfo {
-  int key0[kMaxTilePages];   // first key of each page of the tile
-  int keys[kMaxTilePages];   // its live keys (0: no such page)
-  int clo;                   // first chunk loaded
-  int len;                   // keys of the sequence
+  int2 box[kMaxTilePages];  // first key of each box of the tile, and its live keys (0: no such page)
+  int len;                  // keys of the sequence
+  int clo;                  // first chunk loaded
+  int flags;                // kFirst, kLast, kEnd
+  int slot;                 // partial slot of the CTA, -1: the whole sequence, write the output
   int b, hk;
-  int flags;                 // kFirst, kLast, kEnd
-  int slot;                  // partial slot of the CTA, -1: the whole sequence, write the output
 };
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;
 
@@ -75,8 +80,8 @@ struct PdShared {
   int w[kMaxPairs];
   int abort;
   long long scan[kPdThreads / 32];
-  int start_b, start_ok;
-  long long start_base, total;
+  int start_b, start_len;  // the sequence that this CTA's piece begins in (-1: no piece)
+  long long start_base;
   float mw[kPdConsumers][8], lw[kPdConsumers][8];
 };
 
@@ -113,10 +118,10 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeParams& p, int len) {
 
 // Weight of tiles [0, t) of a sequence in 32-byte reads a key: value row plus
 // live key chunks.  Chunk c is out of reach of the whole tiles before (len - W -
-// 1) / 128, W the window of its last pair.  A list of pages weighs full rows.
+// 1) / 64, W the window of its last pair.  A list of pages weighs full rows.
 template <int NC>
-__device__ __forceinline__ long long tile_weight(const PagedDecodeParams& p, const int* w, int len, int t) {
-  long long x = 2LL * NC * t;
+__device__ __forceinline__ int tile_weight(const PagedDecodeParams& p, const int* w, int len, int t) {
+  int x = 2 * NC * t;
   if (!p.selected) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) x -= min(t, max(0, (len - w[8 * c + 7] - 1) / kTileKeys));
@@ -126,16 +131,72 @@ __device__ __forceinline__ long long tile_weight(const PagedDecodeParams& p, con
 
 // Smallest t in [0, tiles] with tile_weight(t) >= x.
 template <int NC>
-__device__ __forceinline__ int tile_at(const PagedDecodeParams& p, const int* w, int len, int tiles, long long x) {
+__device__ __forceinline__ int tile_at(const PagedDecodeParams& p, const int* w, int len, int tiles, int x) {
+  int dead[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, (len - w[8 * c + 7] - 1) / kTileKeys);
   int lo = 0, hi = tiles;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (tile_weight<NC>(p, w, len, mid) >= x)
+    int y = 2 * NC * mid;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) y -= min(mid, dead[c]);
+    if (y >= x)
       hi = mid;
     else
       lo = mid + 1;
   }
   return lo;
+}
+
+// floor(total * j / kPagedCtas): where the piece of CTA j begins.
+__device__ __forceinline__ long long piece_begin(long long total, int j) {
+  return total / kPagedCtas * j + total % kPagedCtas * j / kPagedCtas;
+}
+
+// A stage of the ring and the parity of its next phase.
+template <int N>
+struct RingPos {
+  int st = 0;
+  uint32_t parity = 0;
+  __device__ void next() {
+    if (++st == N) st = 0, parity ^= 1;
+  }
+};
+
+// S^T of a warp's 16 keys over the chunks CLO..NC-1, the first `dirty` chunks
+// masked by their pairs' windows.  Every load is issued before the first product.
+template <int NC, int CLO>
+__device__ __forceinline__ void qk_tile(float* s, uint32_t at, uint32_t cbytes, uint32_t odd, const uint32_t (*qf)[2], int dirty,
+                                        int far, const int* w, int krow, int kcol) {
+  uint32_t a[NC - CLO][4];
+#pragma unroll
+  for (int j = 0; j < NC - CLO; ++j) ldsm_x4((at + j * cbytes) ^ ((j & 1) ? odd : 0u), a[j]);
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NC - CLO; ++j) {
+    constexpr int c0 = CLO;
+    const int c = c0 + j;
+    if (c < dirty) {  // some pair of the chunk is out of reach of some key
+      const int wl = w[8 * c + kcol], wh = w[8 * c + 4 + kcol];
+      if (far - krow > wl) a[j][0] = 0u;
+      if (far - krow - 8 > wl) a[j][1] = 0u;
+      if (far - krow > wh) a[j][2] = 0u;
+      if (far - krow - 8 > wh) a[j][3] = 0u;
+    }
+    mma_bf16_16816((j & 1) ? t : s, a[j], qf[c][0], qf[c][1]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] += t[e];
+}
+
+template <int NC, int CLO>
+__device__ __forceinline__ void qk_from(int clo, float* s, uint32_t at, uint32_t cbytes, uint32_t odd,
+                                        const uint32_t (*qf)[2], int dirty, int far, const int* w, int krow, int kcol) {
+  if constexpr (CLO < NC - 1) {
+    if (clo != CLO) return qk_from<NC, CLO + 1>(clo, s, at, cbytes, odd, qf, dirty, far, w, krow, kcol);
+  }
+  qk_tile<NC, CLO>(s, at, cbytes, odd, qf, dirty, far, w, krow, kcol);
 }
 
 }  // namespace
@@ -153,8 +214,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   PdShared<D>* sh = reinterpret_cast<PdShared<D>*>(reinterpret_cast<uint8_t*>(sO) + C::MERGE);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = blockIdx.x, ncta = gridDim.x;
+  const int cta = blockIdx.x;
   const int G = p.hq / p.hkv;
+  const int box_log2 = min(p.page_log2, kTileLog2), box = 1 << box_log2;  // keys of a TMA box
 
   if (tid == 0) {
     for (int s = 0; s < NSTG; ++s) {
@@ -164,21 +226,22 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     mbar_init(&sh->join[0], kPdConsumers);
     mbar_init(&sh->join[1], kPdConsumers);
     sh->abort = 0;
-    sh->start_ok = 0;
+    sh->start_b = -1;
     fence_mbar_init();
   }
   if (tid == kPdConsumers * 32) prefetch_tmap(&tm_k), prefetch_tmap(&tm_v);
   for (int i = tid; i < kMaxPairs; i += kPdThreads) sh->w[i] = p.win.w[i];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __syncthreads();
 
   // ---- where this CTA's piece of the tile list begins
   const int per = (p.batch + kPdThreads - 1) / kPdThreads;  // sequences a thread sums
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  const int len0 = b0 < b1 ? clamped_len(p, b0) : 0;
+  __syncthreads();
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const int len = clamped_len(p, b);
-    mine += tile_weight<NC>(p, sh->w, len, tiles_of(p, len)) * p.hkv;
+    const int len = b == b0 ? len0 : clamped_len(p, b);
+    mine += static_cast<long long>(tile_weight<NC>(p, sh->w, len, tiles_of(p, len))) * p.hkv;
   }
   long long incl = mine;
 #pragma unroll
@@ -189,21 +252,21 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   if (lane == 31) sh->scan[warp] = incl;
   __syncthreads();
   long long total = 0, before = incl - mine;
+#pragma unroll
   for (int i = 0; i < kPdThreads / 32; ++i) {
     if (i < warp) before += sh->scan[i];
     total += sh->scan[i];
   }
-  const long long from = total / ncta * cta + total % ncta * cta / ncta;
-  const long long to = total / ncta * (cta + 1) + total % ncta * (cta + 1) / ncta;
+  const long long from = piece_begin(total, cta), to = piece_begin(total, cta + 1);
   if (from < to && from >= before && from < before + mine) {
     long long base = before;
     for (int b = b0; b < b1; ++b) {
-      const int len = clamped_len(p, b);
-      const long long x = tile_weight<NC>(p, sh->w, len, tiles_of(p, len)) * p.hkv;
+      const int len = b == b0 ? len0 : clamped_len(p, b);
+      const long long x = static_cast<long long>(tile_weight<NC>(p, sh->w, len, tiles_of(p, len))) * p.hkv;
       if (from < base + x) {
         sh->start_b = b;
+        sh->start_len = len;
         sh->start_base = base;
-        sh->start_ok = 1;
         break;
       }
       base += x;
@@ -211,27 +274,23 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   }
   __syncthreads();
 
-  if (warp == kPdConsumers) {
+  if (warp >= kPdConsumers) {
     // ================================================================ producer
-    int it = 0;              // stages filled
-    bool ok = true, has_partial0 = false;
-    int meta_b = -1, meta_hk = 0, meta_last = 0;
-    const int ps = 1 << p.page_log2, ppt = kTileKeys >> p.page_log2;
-    int b = sh->start_b, hk = 0;
-    long long base = sh->start_base;  // weight before (b, hk)
-    bool more = sh->start_ok != 0;
-    if (more) {
-      const int len = clamped_len(p, b);
-      const long long unit = tile_weight<NC>(p, sh->w, len, tiles_of(p, len));
-      hk = static_cast<int>((from - base) / unit);
-      base += unit * hk;
-    }
+    RingPos<NSTG> ring;
+    const int pw = warp - kPdConsumers;
+    int it = 0;  // stages passed
+    bool ok = true, has_partial0 = false, has_meta = false;
+    const int ps = 1 << p.page_log2, sub_log2 = p.page_log2 - box_log2, boxes = kTileKeys >> box_log2;
+    const uint32_t box_bytes = static_cast<uint32_t>(D * 2) << box_log2;
+    int b = sh->start_b, hk = 0, len = sh->start_len;
+    bool more = b >= 0;
+    long long base = more ? sh->start_base : 0;  // weight before (b, hk)
     while (more && ok) {
-      const int len = clamped_len(p, b);
       const int tiles = tiles_of(p, len);
-      const long long unit = tile_weight<NC>(p, sh->w, len, tiles);
-      const int t0 = from > base ? tile_at<NC>(p, sh->w, len, tiles, from - base) : 0;
-      const int t1 = to >= base + unit ? tiles : tile_at<NC>(p, sh->w, len, tiles, to - base);
+      const int unit = tile_weight<NC>(p, sh->w, len, tiles);
+      while (from >= base + unit) base += unit, ++hk;  // heads before the piece, at its beginning only
+      const int t0 = from > base ? tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(from - base)) : 0;
+      const int t1 = to >= base + unit ? tiles : tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
         int slot = -1;
         if (t0 > 0) {
@@ -239,119 +298,134 @@ __global__ void __launch_bounds__(kPdThreads, 1)
           has_partial0 = true;
         } else if (t1 < tiles) {
           slot = 1;
+          has_meta = true;
           const long long x = base + tile_weight<NC>(p, sh->w, len, tiles - 1);  // where its last tile begins
-          meta_b = b;
-          meta_hk = hk;
-          // the CTA whose piece holds x: the largest j with floor(j * total / ncta) <= x
-          int lo = cta, hi = ncta - 1;
+          // the CTA whose piece holds x: the largest j with piece_begin(j) <= x
+          int lo = cta, hi = kPagedCtas - 1;
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (total / ncta * mid + total % ncta * mid / ncta <= x)
+            if (piece_begin(total, mid) <= x)
               lo = mid;
             else
               hi = mid - 1;
           }
-          meta_last = lo;
-          if (lane == 0) p.meta[cta] = make_int4(meta_b, meta_hk, meta_last, 0);
+          if (pw == 0 && lane == 0) p.meta[cta] = make_int4(b, hk, lo, 0);
         }
         const int pages = (len + ps - 1) >> p.page_log2;
         const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
         const int count = list ? min(p.n_sel, pages) : pages;
         const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
-        // this lane's page of a tile: logical index (-1: none) and index in the pool
-        auto look_up = [&](int t, int& logical, int& page) {
-          const int i = t * ppt + lane;
-          logical = page = -1;
-          if (lane < ppt && i < count) {
-            logical = list ? list[i] : i;
-            if (logical >= pages) {
-              atomicCAS(p.err, 0u, kErrBadSelect);
-              logical = -1;
+        // 32 boxes at a time, a lane each: of the group in use the page in the
+        // sequence (-1: none) and in the pool, and, on their way, the next group's
+        // entries of the table and the list entries of the one after it
+        const int end = t1 * boxes;
+        auto listed = [&](int i) {  // page of box i in the sequence
+          const int k = i >> sub_log2;
+          return i < end && k < count ? (list ? list[k] : k) : -1;
+        };
+        auto in_pool = [&](int& logical) {  // its page in the pool, not yet looked at
+          if (logical >= pages) {
+            atomicCAS(p.err, 0u, kErrBadSelect);
+            logical = -1;
+          }
+          return logical >= 0 ? table[logical] : 0;
+        };
+        int logical_next = listed(t0 * boxes + lane);
+        int page_next = in_pool(logical_next);
+        int logical_far = listed(t0 * boxes + 32 + lane);
+        for (int tg = t0; tg < t1 && ok; tg += 32 >> (kTileLog2 - box_log2)) {
+          // this lane's box of the group
+          const int i = tg * boxes + lane;
+          int logical = logical_next, page = page_next;
+          logical_next = logical_far;
+          page_next = in_pool(logical_next);
+          logical_far = listed(i + 64);
+          if (logical >= 0 && (page < 0 || page >= p.num_pages)) {
+            atomicCAS(p.err, 0u, kErrBadPage);
+            logical = -1;
+          }
+          const int slot0 = (i & ((1 << sub_log2) - 1)) << box_log2;  // its first slot
+          const int key0 = (max(logical, 0) << p.page_log2) + slot0;
+          const int keys = logical >= 0 ? max(0, min(box, len - key0)) : 0;
+          const int row = page * p.hkv + hk;
+          int near = keys > 0 ? key0 + keys - 1 : -1;  // last key of the box, then of its tile
+          int live = keys > 0;                         // boxes of its tile to be loaded
+          for (int off = 1; off < boxes; off <<= 1) {
+            near = max(near, __shfl_xor_sync(0xffffffffu, near, off));
+            live += __shfl_xor_sync(0xffffffffu, live, off);
+          }
+          int clo = 0;  // windows grow with the chunk: the chunks out of reach are the first ones
+          if (near >= 0) {
+#pragma unroll
+            for (int c = 0; c < NC - 1; ++c) clo += sh->w[8 * c + 7] < len - 1 - near;
+          }
+          const int tile = i >> (kTileLog2 - box_log2);  // the tile of this lane's box
+          const bool lead = (lane & (boxes - 1)) == 0;
+          const int tg1 = min(t1, tg + (32 >> (kTileLog2 - box_log2)));
+          for (int t = tg; t < tg1; ++t, ++it, ring.next()) {
+            if (it % kPdProducers != pw) continue;
+            if (it >= NSTG && !warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x501)) {
+              ok = false;
+              break;
             }
-            if (logical >= 0) {
-              page = table[logical];
-              if (page < 0 || page >= p.num_pages) {
-                atomicCAS(p.err, 0u, kErrBadPage);
-                logical = -1;
+            StageInfo* info = &sh->info[ring.st];
+            if (tile == t) {
+              info->box[lane & (boxes - 1)] = make_int2(key0, keys);
+              if (lead) {
+                info->len = len;
+                info->clo = clo;
+                info->flags = (t == t0 ? kFirst : 0) | (t + 1 == t1 ? kLast : 0);
+                info->slot = slot;
+                info->b = b;
+                info->hk = hk;
+              }
+            }
+            __syncwarp();
+            uint8_t* stg = sStage + ring.st * C::STAGE;
+            uint64_t* full = &sh->full[ring.st];
+            if (tile == t) {
+              if (lead) {
+                const uint32_t q_bytes = t == t0 ? G * D * 2 : 0;
+                mbar_arrive_expect_tx(full, live * 2 * box_bytes + q_bytes);
+                if (q_bytes)
+                  bulk_load(sQ + ring.st * C::Q,
+                            static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride + static_cast<long long>(hk) * G * D,
+                            q_bytes, full);
+              }
+              if (keys > 0) {
+                uint8_t* dst = stg + (lane & (boxes - 1)) * box_bytes;
+                tma_load_4d(dst, &tm_k, full, 0, slot0 >> 2, clo, row);
+                tma_load_4d(dst + C::HALF, &tm_v, full, 0, slot0, 0, row);
               }
             }
           }
-        };
-        int logical, page;
-        look_up(t0, logical, page);
-        for (int t = t0; t < t1; ++t) {
-          int logical_next = -1, page_next = -1;
-          if (t + 1 < t1) look_up(t + 1, logical_next, page_next);
-          const int st = it % NSTG;
-          if (it >= NSTG && !warp_wait(&sh->empty[st], ((it / NSTG) - 1) & 1, &sh->abort, p.err, 0x501)) {
-            ok = false;
-            break;
-          }
-          StageInfo* info = &sh->info[st];
-          const int key0 = max(logical, 0) << p.page_log2;
-          const int keys = logical >= 0 ? min(ps, len - key0) : 0;
-          const int near = __reduce_max_sync(0xffffffffu, keys > 0 ? key0 + keys - 1 : -1);
-          int clo = 0;
-          if (near >= 0)
-            while (clo < NC - 1 && sh->w[8 * clo + 7] < len - 1 - near) ++clo;
-          if (lane < ppt) {
-            info->key0[lane] = key0;
-            info->keys[lane] = keys;
-          }
-          const unsigned live = __ballot_sync(0xffffffffu, keys > 0);
-          const bool first = t == t0;
-          if (lane == 0) {
-            info->clo = clo;
-            info->len = len;
-            info->b = b;
-            info->hk = hk;
-            info->flags = (first ? kFirst : 0) | (t + 1 == t1 ? kLast : 0);
-            info->slot = slot;
-          }
-          __syncwarp();
-          uint8_t* stg = sStage + st * C::STAGE;
-          if (lane == 0) {
-            const uint32_t q_bytes = G * D * 2;
-            mbar_arrive_expect_tx(&sh->full[st], __popc(live) * 2 * ps * D * 2 + (first ? q_bytes : 0));
-            if (first)
-              bulk_load(sQ + st * C::Q,
-                        static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride + static_cast<long long>(hk) * G * D, q_bytes,
-                        &sh->full[st]);
-          }
-          __syncwarp();
-          if (keys > 0) {
-            const int row = page * p.hkv + hk;
-            tma_load_4d(stg + lane * ps * D * 2, &tm_k, &sh->full[st], 0, 0, clo, row);
-            tma_load_4d(stg + C::HALF + lane * ps * D * 2, &tm_v, &sh->full[st], 0, 0, 0, row);
-          }
-          logical = logical_next;
-          page = page_next;
-          ++it;
         }
       }
       base += unit;
-      if (++hk == p.hkv) hk = 0, ++b;
+      if (++hk == p.hkv) {
+        hk = 0;
+        if (++b < p.batch && base < to) len = clamped_len(p, b);
+      }
       more = b < p.batch && base < to;
     }
-    if (ok) {  // the end mark
-      const int st = it % NSTG;
-      if (it >= NSTG) ok = warp_wait(&sh->empty[st], ((it / NSTG) - 1) & 1, &sh->abort, p.err, 0x502);
+    if (ok && it % kPdProducers == pw) {  // the end mark
+      if (it >= NSTG) ok = warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x502);
       if (ok && lane == 0) {
-        sh->info[st].flags = kEnd;
-        mbar_arrive(&sh->full[st]);
+        sh->info[ring.st].flags = kEnd;
+        mbar_arrive(&sh->full[ring.st]);
       }
     }
-    if (lane == 0 && meta_b < 0) p.meta[cta] = make_int4(-1, 0, 0, 0);
-    if (!has_partial0 && lane < G) {  // no piece of an earlier CTA's sequence here
+    if (pw == 0 && lane == 0 && !has_meta) p.meta[cta] = make_int4(-1, 0, 0, 0);
+    if (pw == 0 && !has_partial0 && lane < G) {  // no piece of an earlier CTA's sequence here
       float* part = p.partials + (static_cast<long long>(cta) * 2 * 8 + lane) * (D + 2);
       part[D] = -INFINITY;
       part[D + 1] = 0.f;
     }
-    if (!ok && lane == 0) {  // wait (bounded) for the copies in flight
-      for (int s = 0; s < NSTG && s < it; ++s) {
-        const int last = (it - 1 - s) / NSTG * NSTG + s;  // the last fill of stage s
+    if (!ok && lane == 0) {  // wait (bounded) for this warp's copies in flight
+      for (int j = it > NSTG ? it - NSTG : 0; j < it; ++j) {
+        if (j % kPdProducers != pw) continue;
         const long long c0 = clock64();
-        while (!mbar_try_wait(&sh->full[s], (last / NSTG) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        while (!mbar_try_wait(&sh->full[j % NSTG], (j / NSTG) & 1) && clock64() - c0 < kWaitLimitCycles) {
         }
       }
     }
@@ -361,11 +435,24 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   // ================================================================ consumers
   const float scale = kLog2e * rsqrtf(static_cast<float>(D));
   const int kcol = lane & 3, krow = lane >> 2;  // this lane's pair in a half chunk / head pair, and key row / dim row
-  const int psmask = (1 << p.page_log2) - 1, pbytes = D * 2 << p.page_log2, cbytes = 32 << p.page_log2;
+  const int group = warp >> 2;
+  // this warp's 16 keys of a tile: box and slot in it
+  const int bx = (16 * (warp & 3)) >> box_log2, off = (16 * (warp & 3)) & (box - 1);
+  const uint32_t cbytes = 32u << box_log2, vhalf = 128u << box_log2;
+  const int krow_ld = off + (lane & 15), vrow_ld = off + (lane & 7) + ((lane >> 4) << 3);
+  // a chunk's rows of four keys, 128 bytes each, lie 16-byte units swizzled by the
+  // row's number in its 1024 bytes; chunks of 16 keys are half as long, so every
+  // other one starts at row 4
+  const uint32_t k_at = bx * (static_cast<uint32_t>(D * 2) << box_log2) + (krow_ld >> 2) * 128 +
+                        ((((krow_ld & 3) * 2 + (lane >> 4)) ^ ((krow_ld >> 2) & 7)) << 4);
+  const uint32_t k_odd = box == 16 ? 64u : 0u;
+  const uint32_t v_at = C::HALF + bx * (static_cast<uint32_t>(D * 2) << box_log2) + vrow_ld * 128;
   uint32_t qf[NC][2];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2*kcol, 2*kcol + 1
   float o[D / 16][4];  // O^T: dims 16u + krow (+8), heads 2*kcol (+1)
+  const int w_first = lane < NC ? sh->w[8 * lane] : 0x7fffffff;  // smallest window of chunk `lane`
   int joins = 0;
+  RingPos<NSTG> ring;
   // a bounded wait, so that a warp that gave up does not hold the others
   auto meet = [&](int which) {
     __syncwarp();
@@ -373,8 +460,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     return warp_wait(&sh->join[which], joins & 1, &sh->abort, p.err, 0x504);
   };
   for (int it = 0;; ++it) {
-    const int st = it % NSTG;
-    if (!warp_wait(&sh->full[st], (it / NSTG) & 1, &sh->abort, p.err, 0x503)) return;
+    const int st = ring.st;
+    if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x503)) return;
+    ring.next();
     const StageInfo* info = &sh->info[st];
     const int flags = info->flags;
     if (flags & kEnd) return;
@@ -389,94 +477,73 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
       for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     }
-    const int clo = info->clo, qpos = info->len - 1;
-    const uint32_t stg = smem_u32(sStage + st * C::STAGE);
+    if ((it & 1) == group) {
+      const int2 my = info->box[bx];
+      const int live = my.y - off;                      // live keys from this warp's first on
+      const int far = info->len - 1 - (my.x + off);  // distance of its first key
+      const uint32_t stg = smem_u32(sStage + st * C::STAGE);
 
-    // ---- S^T of this warp's 32 keys, pairs beyond their window zeroed
-    float s[2][4];
-    int live[2];  // live keys from this 16-key block's first on
-    uint32_t blk[2];  // page offset and slot of the block
+      // ---- S^T of 16 keys, pairs beyond their window zeroed
+      const int dirty = __popc(__ballot_sync(0xffffffffu, far > w_first));
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      qk_from<NC, 0>(info->clo, s, stg + k_at, cbytes, k_odd, qf, dirty, far, sh->w, krow, kcol);
+      // the values' first half is fetched while the softmax runs
+      uint32_t va[D / 32][4];
+      auto load_v = [&](int u0) {
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const int j = 32 * warp + 16 * mt, pg = j >> p.page_log2, off = j & psmask;
-      live[mt] = info->keys[pg] - off;
-      blk[mt] = static_cast<uint32_t>(pg * pbytes) | static_cast<uint32_t>(off) << 24;
-      const int far = qpos - (info->key0[pg] + off);  // distance of the block's first key
-      s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
-      const int row = off + (lane & 7) + (lane & 8);
-      const uint32_t ka = stg + pg * pbytes + row * 32 + (((lane >> 4) ^ ((row >> 2) & 1)) << 4);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (c < clo) continue;
-        uint32_t a[4];
-        ldsm_x4(ka + (c - clo) * cbytes, a);
-        if (far > sh->w[8 * c]) {  // some pair of the chunk is out of reach of some key
-          const int wl = sh->w[8 * c + kcol], wh = sh->w[8 * c + 4 + kcol];
-          if (far - krow > wl) a[0] = 0u;
-          if (far - krow - 8 > wl) a[1] = 0u;
-          if (far - krow > wh) a[2] = 0u;
-          if (far - krow - 8 > wh) a[3] = 0u;
+        for (int u = 0; u < D / 32; ++u) {
+          const int dim = 16 * (u0 + u) + (lane & 8);
+          ldsm_x4_t(stg + v_at + ((u0 + u) >> 2) * vhalf + ((((dim & 63) >> 3) ^ (vrow_ld & 7)) << 4), va[u]);
         }
-        mma_bf16_16816(s[mt], a, qf[c][0], qf[c][1]);
+      };
+      load_v(0);
+      // ---- online softmax of heads 2*kcol, 2*kcol + 1
+      float mu[2], corr[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[e] = krow < live ? s[e] * scale : -INFINITY;
+        s[e + 2] = krow + 8 < live ? s[e + 2] * scale : -INFINITY;
+        float mx = fmaxf(s[e], s[e + 2]);
+#pragma unroll
+        for (int sh_ = 4; sh_ < 32; sh_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh_));
+        const float mn = fmaxf(m[e], mx);
+        mu[e] = mn == -INFINITY ? 0.f : mn;  // no live key yet
+        corr[e] = ex2_approx(m[e] - mu[e]);
+        m[e] = mn;
+        l[e] *= corr[e];
       }
-    }
-    // ---- online softmax of heads 2*kcol, 2*kcol + 1
-    float mx[2] = {-INFINITY, -INFINITY};
+      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+        for (int u = 0; u < D / 16; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[mt][e] = krow + (e & 2) * 4 < live[mt] ? s[mt][e] * scale : -INFINITY;
-        mx[e & 1] = fmaxf(mx[e & 1], s[mt][e]);
+          for (int e = 0; e < 4; ++e) o[u][e] *= corr[e & 1];
       }
-    float mu[2], corr[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
-      const float mn = fmaxf(m[e], mx[e]);
-      mu[e] = mn == -INFINITY ? 0.f : mn;  // no live key yet
-      corr[e] = ex2_approx(m[e] - mu[e]);
-      m[e] = mn;
-      l[e] *= corr[e];
-    }
-    if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-      for (int u = 0; u < D / 16; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[u][e] *= corr[e & 1];
-    }
-    uint32_t pb[2][2];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        pr[e] = ex2_approx(s[mt][e] - mu[e & 1]);
+        pr[e] = ex2_approx(s[e] - mu[e & 1]);
         l[e & 1] += pr[e];
       }
-      pb[mt][0] = movmatrix_t(pack_bf16x2(pr[0], pr[1]));
-      pb[mt][1] = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
-    }
-    // ---- O^T += V^T P^T
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const int key = static_cast<int>(blk[mt] >> 24) + (lane & 7) + ((lane >> 4) << 3);
-      const uint32_t va = stg + C::HALF + (blk[mt] & 0xFFFFFFu);
+      const uint32_t pb0 = movmatrix_t(pack_bf16x2(pr[0], pr[1])), pb1 = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
+      // ---- O^T += V^T P^T
       // rows behind the last key may hold anything: their values count as zero
-      const int n = live[mt] - 2 * kcol;
+      const int n = live - 2 * kcol;
       const uint32_t keep0 = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u;
       const uint32_t keep1 = n >= 10 ? 0xFFFFFFFFu : n == 9 ? 0xFFFFu : 0u;
 #pragma unroll
-      for (int u = 0; u < D / 16; ++u) {
-        const int dim = 16 * u + (lane & 8);
-        uint32_t a[4];
-        ldsm_x4_t(va + (dim >> 6) * (128 << p.page_log2) + key * 128 + ((((dim & 63) >> 3) ^ (key & 7)) << 4), a);
-        a[0] &= keep0;
-        a[1] &= keep0;
-        a[2] &= keep1;
-        a[3] &= keep1;
-        mma_bf16_16816(o[u], a, pb[mt][0], pb[mt][1]);
+      for (int half = 0; half < 2; ++half) {
+        if (half) load_v(D / 32);
+        if (live < 16) {
+#pragma unroll
+          for (int u = 0; u < D / 32; ++u) {
+            va[u][0] &= keep0;
+            va[u][1] &= keep0;
+            va[u][2] &= keep1;
+            va[u][3] &= keep1;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) mma_bf16_16816(o[half * (D / 32) + u], va[u], pb0, pb1);
       }
     }
     const int b = info->b, hk = info->hk, slot = info->slot;
@@ -484,11 +551,11 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     if (lane == 0) mbar_arrive(&sh->empty[st]);
     if (!(flags & kLast)) continue;
 
-    // ---- join the four warps
+    // ---- join the warps
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+      for (int sh_ = 4; sh_ < 32; sh_ <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh_);
       if (krow == 0) {
         sh->mw[warp][2 * kcol + e] = m[e];
         sh->lw[warp][2 * kcol + e] = l[e];
@@ -498,7 +565,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     for (int u = 0; u < D / 16; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sO[(warp * 8 + 2 * kcol + (e & 1)) * C::OROW + 16 * u + krow + (e & 2) * 4] = o[u][e];
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (!meet(0)) return;
     for (int i = tid; i < G * D; i += kPdConsumers * 32) {
       const int g = i / D, e = i % D;
       float M = -INFINITY;
@@ -531,24 +598,60 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 
 // Joins the pieces of the sequence and head that CTA blockIdx.x began and did not
 // end: its slot 1 and slot 0 of the CTAs up to meta.z.  blockIdx.y = query head.
+// The scales of all pieces are found first, side by side, so that the sums over
+// them wait for no load twice.
 template <int D>
-__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(2 * D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ float s_f[kPagedCtas], s_red[2 * D / 32], s_acc[D], s_sum[2 * D / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 meta = p.meta[blockIdx.x];
-  const int G = p.hq / p.hkv, g = blockIdx.y, e = threadIdx.x;
   if (meta.x < 0) return;
+  const int G = p.hq / p.hkv, g = blockIdx.y, tid = threadIdx.x;
   const int first = blockIdx.x, n = meta.z - first + 1;
   auto part = [&](int i) { return p.partials + ((static_cast<long long>(first + i) * 2 + (i == 0)) * 8 + g) * (D + 2); };
-  float M = -INFINITY;
-  for (int i = 0; i < n; ++i) M = fmaxf(M, part(i)[D]);
-  float a = 0.f, l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float mi = part(i)[D];
-    if (mi == -INFINITY) continue;
-    const float f = ex2_approx(mi - M);
-    a += part(i)[e] * f;
-    l += part(i)[D + 1] * f;
+  constexpr int kPer = (kPagedCtas + 2 * D - 1) / (2 * D);
+  float mi[kPer], li[kPer], M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid + k * 2 * D;
+    mi[k] = i < n ? part(i)[D] : -INFINITY;
+    li[k] = i < n ? part(i)[D + 1] : 0.f;
+    M = fmaxf(M, mi[k]);
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2 * D / 32; ++w) M = fmaxf(M, s_red[w]);
+  float l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid + k * 2 * D;
+    const float f = mi[k] == -INFINITY ? 0.f : ex2_approx(mi[k] - M);
+    if (i < n) s_f[i] = f;
+    l += li[k] * f;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  if ((tid & 31) == 0) s_sum[tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 2 * D / 32; ++w) l += s_sum[w];
+  // two halves of the block take every other piece
+  const int e = tid % D;
+  float a = 0.f;
+#pragma unroll 8
+  for (int i = tid / D; i < n; i += 2) {
+    const float f = s_f[i];
+    const float x = f > 0.f ? part(i)[e] : 0.f;  // an empty piece holds no sums
+    a += x * f;
+  }
+  if (tid >= D) s_acc[e] = a;
+  __syncthreads();
+  if (tid >= D) return;
+  a += s_acc[e];
   const long long row = static_cast<long long>(meta.x) * p.hq + meta.y * G + g;
   static_cast<__nv_bfloat16*>(p.out)[row * D + e] = __float2bfloat16(M == -INFINITY ? 0.f : a / l);
   if (p.lse && e == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kLn2;
@@ -573,7 +676,7 @@ static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPagedCtas, p.hq / p.hkv);
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(2 * D);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

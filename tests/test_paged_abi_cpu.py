@@ -140,7 +140,7 @@ def test_bindings_refuse_wrong_tensors():
 
 # ------------------------------------------------------------------ the decode's division of its work
 
-CTAS, TILE = 148, 128
+CTAS, TILE = 148, 64
 
 
 def _cdiv0(a, b):  # C's division, towards zero
