@@ -426,56 +426,29 @@ def fasa_decode(q_rot, k_chunked, v, kv_len, pair_mask, budget, selected=None, s
     return out
 
 
-def _head_rows(name, x, dtype, heads=None, d=None):
-    """Token stride of x [T][H][d], whose heads are contiguous (a slice of a fused projection is fine)."""
-    if x.dim() != 3 or x.dtype != dtype or (heads or x.shape[1]) != x.shape[1] or (d or x.shape[2]) != x.shape[2]:
-        raise TypeError(f"{name}: a [tokens][heads][d] tensor of {dtype} is expected, got {tuple(x.shape)} {x.dtype}")
-    T, H, n = x.shape
-    st = x.stride()
-    if T * H * n and (st[2] != 1 or (H > 1 and st[1] != n)):
-        raise TypeError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if T > 1 else H * n
+_calls = None
 
 
-def _dense(name, x, dtype, shape):
-    """x must be contiguous, of this type and shape (None: any extent)."""
-    if x.dtype != dtype or x.dim() != len(shape) or not x.is_contiguous() or any(
-            n is not None and n != m for n, m in zip(shape, x.shape)):
-        raise TypeError(f"{name}: a contiguous {dtype} tensor of shape {shape} is expected, "
-                        f"got {tuple(x.shape)} {x.dtype}")
-    return x
+def _tensor_calls():
+    """The compiled checks and calls on torch tensors (csrc/tensor_calls.cpp), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
 
+        import torch  # noqa: F401  the module links to its libraries
 
-def _on(device, **tensors):
-    for name, x in tensors.items():
-        if x is not None and x.device != device:
-            raise TypeError(f"{name} is on {x.device}, the queries or keys on {device}")
-
-
-def _launch(fn, args, device, stream):
-    """fn(args) on the tensors' device, on `stream` or that device's current one."""
-    import torch
-
-    if device.type != "cuda":
-        raise TypeError(f"tensors of a CUDA device are expected, got {device}")
-    if device.index == torch.cuda.current_device():
-        fn(args, stream)
-    else:
-        with torch.cuda.device(device):
-            fn(args, stream)
-
-
-def _positions(pos, tokens, pair_axis):
-    """(axes, pair_axis bytes) of positions [axes][tokens] int64 (None: the slots)."""
-    import torch
-
-    if pos is not None:
-        _dense("pos", pos, torch.int64, (None, tokens))
-    return (1 if pos is None else pos.shape[0]), (None if pair_axis is None else bytes(pair_axis))
-
-
-def _weight(name, w, dtype, d):
-    return None if w is None else _dense(name, w, dtype, (d,)).data_ptr()
+        lib = load_library()
+        path = os.path.join(_HERE, "_tensor_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run __graft_entry__.build() "
+                               "(or python -m rope_frequency_sparse_b200.build)")
+        loader = importlib.machinery.ExtensionFileLoader("_tensor_calls", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensor_calls", loader))
+        loader.exec_module(module)
+        module.bind(lib._handle, _check)
+        _calls = module
+    return _calls
 
 
 def qk_norm_rope(q, k, theta, pos, q_weight=None, k_weight=None, eps=1e-6, pair_axis=None,
@@ -483,42 +456,8 @@ def qk_norm_rope(q, k, theta, pos, q_weight=None, k_weight=None, eps=1e-6, pair_
     """Norms of queries q [T][Hq][d] and keys k [T][Hkv][d] (bf16 or fp32; token strides as they are) for each
     head, and the rotation by pos [axes][T] (int64), pair i by axis pair_axis[i].  Returns (q_out, k_out),
     contiguous, pair i in dims (2i, 2i+1)."""
-    import torch
-
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    qs, ks = _head_rows("q", q, q.dtype), _head_rows("k", k, q.dtype, d=d)
-    code = dtype_code(q)
-    if k.shape[0] != T:
-        raise TypeError(f"q has {T} tokens, k {k.shape[0]}")
-    if pair_axis is not None and len(pair_axis) != d // 2:
-        raise TypeError(f"pair_axis: {d // 2} entries are expected, got {len(pair_axis)}")
-    axes, axis = _positions(pos, T, pair_axis)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device)
-    _dense("q_out", q_out, q.dtype, (T, Hq, d))
-    _dense("k_out", k_out, q.dtype, (T, Hkv, d))
-    _on(q.device, k=k, pos=pos, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
-    a = QkNormRopeArgs(q.data_ptr(), k.data_ptr(), qs, ks, q_out.data_ptr(), k_out.data_ptr(),
-                       _weight("q_weight", q_weight, q.dtype, d), _weight("k_weight", k_weight, q.dtype, d),
-                       _ptr(pos), axis, T, Hq, Hkv, d, axes, pairing, code, theta, eps)
-    _launch(atf_qk_norm_rope, a, q.device, stream)
-    return q_out, k_out
-
-
-def _pool(k_pages, v_pages, page_table):
-    """(num_pages, kv heads, d, page size, batch, max_pages) of a paged cache."""
-    import torch
-
-    if k_pages.dim() != 5:
-        raise TypeError(f"k_pages: [pages][kv heads][d/16][page size][16] is expected, got {tuple(k_pages.shape)}")
-    N, Hkv, nc, ps, _ = k_pages.shape
-    _dense("k_pages", k_pages, torch.bfloat16, (N, Hkv, nc, ps, 16))
-    _dense("v_pages", v_pages, torch.bfloat16, (N, Hkv, ps, nc * 16))
-    _dense("page_table", page_table, torch.int32, (None, None))
-    return N, Hkv, nc * 16, ps, page_table.shape[0], page_table.shape[1]
+    return (_calls or _tensor_calls()).qk_norm_rope(q, k, theta, pos, q_weight, k_weight, eps, pair_axis, pairing, q_out,
+                                                    k_out, stream)
 
 
 def paged_append(q, k, v, k_pages, v_pages, page_table, start, theta, cu=None, pos=None, q_weight=None,
@@ -527,67 +466,16 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, start, theta, cu=None, p
     """Append new tokens' k, v [T][Hkv][d] to the pages of their sequences (k normed and rotated) and return their
     queries q [T][Hq][d] (or None) normed and rotated, [T][Hq][d].  start [B] int32: tokens each sequence
     holds; cu [B + 1] int32: its rows of k and v (None: one each)."""
-    import torch
-
-    N, Hkv, d, ps, B, P = _pool(k_pages, v_pages, page_table)
-    bf16 = torch.bfloat16
-    T = k.shape[0]
-    ks, vs = _head_rows("k", k, bf16, Hkv, d), _head_rows("v", v, bf16, Hkv, d)
-    qs, Hq = 0, Hkv
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise TypeError("q, k and v must have the same tokens")
-    if pair_axis is not None and len(pair_axis) != d // 2:
-        raise TypeError(f"pair_axis: {d // 2} entries are expected, got {len(pair_axis)}")
-    if q is not None:
-        qs, Hq = _head_rows("q", q, bf16, d=d), q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
-        _dense("q_out", q_out, bf16, (T, Hq, d))
-    _dense("start", start, torch.int32, (B,))
-    if cu is not None:
-        _dense("cu", cu, torch.int32, (B + 1,))
-    if bounds is not None:
-        _dense("bounds", bounds, bf16, (N, Hkv, 2, d))
-    axes, axis = _positions(pos, T, pair_axis)
-    _on(k.device, q=q, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, start=start, cu=cu, pos=pos,
-        q_weight=q_weight, k_weight=k_weight, bounds=bounds, q_out=q_out)
-    a = PagedAppendArgs(_ptr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_out), k_pages.data_ptr(),
-                        v_pages.data_ptr(), _ptr(bounds), _weight("q_weight", q_weight, bf16, d),
-                        _weight("k_weight", k_weight, bf16, d), page_table.data_ptr(), start.data_ptr(), _ptr(cu),
-                        _ptr(pos), axis, N, T, B, Hq, Hkv, d, ps, P, axes, pairing, theta, eps)
-    _launch(atf_paged_append, a, k.device, stream)
-    return q_out
+    return (_calls or _tensor_calls()).paged_append(q, k, v, k_pages, v_pages, page_table, start, theta, cu, pos, q_weight,
+                                                    k_weight, eps, pair_axis, pairing, bounds, q_out, stream)
 
 
 def paged_decode(q, k_pages, v_pages, page_table, kv_len, theta, alpha, selected=None, lse=None, out=None,
                  workspace=None, stream=None):
     """Decode step over a paged cache; q [B][Hq][d] (rotated), kv_len [B] int32 on the device; selected
     [B][Hkv][n] int32: attend to these pages only.  Returns out [B][Hq][d]; lse [B][Hq] fp32 is filled if given."""
-    import torch
-
-    N, Hkv, d, ps, B, P = _pool(k_pages, v_pages, page_table)
-    qs, Hq = _head_rows("q", q, torch.bfloat16, d=d), q.shape[1]
-    if q.shape[0] != B:
-        raise TypeError(f"q has {q.shape[0]} sequences, page_table {B}")
-    _dense("kv_len", kv_len, torch.int32, (B,))
-    n_sel = 0
-    if selected is not None:
-        n_sel = _dense("selected", selected, torch.int32, (B, Hkv, None)).shape[2]
-    if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
-    _dense("out", out, torch.bfloat16, (B, Hq, d))
-    if lse is not None:
-        _dense("lse", lse, torch.float32, (B, Hq))
-    if workspace is None:
-        workspace = torch.empty(max(atf_paged_decode_workspace_bytes(B, Hq, Hkv, d), 16), dtype=torch.uint8,
-                                device=q.device)
-    _on(q.device, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_len=kv_len, selected=selected, out=out,
-        lse=lse, workspace=workspace)
-    a = PagedDecodeArgs(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                        kv_len.data_ptr(), _ptr(selected), out.data_ptr(), _ptr(lse), N, B, Hq, Hkv, d, ps, P, n_sel,
-                        theta, alpha, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _launch(atf_paged_decode, a, q.device, stream)
-    return out
+    return (_calls or _tensor_calls()).paged_decode(q, k_pages, v_pages, page_table, kv_len, theta, alpha, selected, lse, out,
+                                                    workspace, stream)
 
 
 def page_select(q, bounds, page_table, kv_len, page_size, n_select, theta, alpha, n_first=1, n_last=1, selected=None,
@@ -595,29 +483,8 @@ def page_select(q, bounds, page_table, kv_len, page_size, n_select, theta, alpha
     """The n_select pages of each sequence and kv head with the highest bound on a logit of q [B][Hq][d]
     (rotated), the first n_first and last n_last pages among them: ascending, -1 behind the last, int32
     [B][Hkv][n_select]."""
-    import torch
-
-    if bounds.dim() != 4:
-        raise TypeError(f"bounds: [pages][kv heads][2][d] is expected, got {tuple(bounds.shape)}")
-    N, Hkv, _, d = bounds.shape
-    _dense("bounds", bounds, torch.bfloat16, (N, Hkv, 2, d))
-    B, P = _dense("page_table", page_table, torch.int32, (None, None)).shape
-    qs, Hq = _head_rows("q", q, torch.bfloat16, d=d), q.shape[1]
-    if q.shape[0] != B:
-        raise TypeError(f"q has {q.shape[0]} sequences, page_table {B}")
-    _dense("kv_len", kv_len, torch.int32, (B,))
-    if selected is None:
-        selected = torch.empty((B, Hkv, n_select), dtype=torch.int32, device=q.device)
-    _dense("selected", selected, torch.int32, (B, Hkv, n_select))
-    if workspace is None:
-        workspace = torch.empty(max(atf_page_select_workspace_bytes(B, Hkv, P), 16), dtype=torch.uint8,
-                                device=q.device)
-    _on(q.device, bounds=bounds, page_table=page_table, kv_len=kv_len, selected=selected, workspace=workspace)
-    a = PageSelectArgs(q.data_ptr(), qs, bounds.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
-                       selected.data_ptr(), N, B, Hq, Hkv, d, page_size, P, n_select, n_first, n_last, theta, alpha,
-                       workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _launch(atf_page_select, a, q.device, stream)
-    return selected
+    return (_calls or _tensor_calls()).page_select(q, bounds, page_table, kv_len, page_size, n_select, theta, alpha, n_first,
+                                                   n_last, selected, workspace, stream)
 
 
 def is_dense(alpha: float) -> bool:

@@ -1,5 +1,6 @@
 """Build step for the CUDA library: compiles csrc/*.cu for sm_100a with nvcc and
-links libatf.so next to this file (in-tree, so it ships with the package)."""
+links libatf.so next to this file (in-tree, so it ships with the package), and
+csrc/tensor_calls.cpp, its calls on torch tensors, to _tensor_calls.so."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -7,12 +8,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatf.so")
+TENSOR_CALLS = os.path.join(HERE, "_tensor_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -43,14 +46,35 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_tensor_calls(force):
+    src = os.path.join(SRC, "tensor_calls.cpp")
+    if not force and not _stale(TENSOR_CALLS, [src, os.path.join(ROOT, "include", "atf.h")]):
+        return
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = TENSOR_CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + d for d in inc), src, "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSOR_CALLS)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(SRC, "*.cu")))
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = ex.submit(_build_tensor_calls, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        calls.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]

@@ -181,8 +181,20 @@ atf_status atf::report_error(atf_status st, const char* fmt, ...) {
 
 atf_status atf::check_method(int d, double theta, double alpha) { return check_params(d, theta, alpha); }
 
-void atf::method_windows(int d, double theta, double alpha, Windows* out, double* omega) {
-  kernel_windows(d, theta, alpha, out, omega);
+void atf::method_windows(int d, double theta, double alpha, Windows* out) {
+  // a thread's calls mostly share the method; the powers take longer than the launch
+  static thread_local struct {
+    int d = 0;
+    double theta = 0.0, alpha = 0.0;
+    Windows win;
+  } last;
+  if (last.d != d || last.theta != theta || last.alpha != alpha) {
+    kernel_windows(d, theta, alpha, &last.win, nullptr);
+    last.d = d;
+    last.theta = theta;
+    last.alpha = alpha;
+  }
+  *out = last.win;
 }
 
 atf_status atf::tensor_map_4d(CUtensorMap* map, const void* base, const unsigned long long dims[4],

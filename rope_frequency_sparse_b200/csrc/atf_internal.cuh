@@ -168,8 +168,8 @@ atf_status report_error(atf_status st, const char* fmt, ...);
 // Checks d, theta and alpha; records a message and returns its status.
 atf_status check_method(int d, double theta, double alpha);
 
-// Windows of the pairs in the kernels' integer domain; omega (kMaxPairs entries) nullable.
-void method_windows(int d, double theta, double alpha, Windows* out, double* omega);
+// Windows of the pairs in the kernels' integer domain.
+void method_windows(int d, double theta, double alpha, Windows* out);
 
 // Tiled tensor map of a 4-D bf16 tensor (dims innermost first, strides of dims
 // 1..3 in bytes); elements outside read as zero.

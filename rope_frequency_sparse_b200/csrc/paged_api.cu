@@ -50,10 +50,19 @@ atf_status rotary_table(const char* who, int d, double theta, int n_axes, const 
   if (n_axes > 1 && !pair_axis)
     return report_error(ATF_ERR_INVALID_ARG, "%s: several position axes need pair_axis", who);
   const double two_pi = 6.283185307179586476925286766559;
+  // a thread's calls mostly share d and theta; the powers take longer than the launch
+  static thread_local struct {
+    int d = 0;
+    double theta = 0.0, turns[kMaxPairs] = {};
+  } last;
+  if (last.d != d || last.theta != theta) {
+    for (int i = 0; i < kMaxPairs; ++i) last.turns[i] = i < d / 2 ? std::pow(theta, -2.0 * i / d) / two_pi : 0.0;
+    last.d = d;
+    last.theta = theta;
+  }
   rot->n_axes = n_axes;
-  for (int i = 0; i < kMaxPairs; ++i) rot->turns[i] = 0.0, rot->axis[i] = 0;
+  for (int i = 0; i < kMaxPairs; ++i) rot->turns[i] = last.turns[i], rot->axis[i] = 0;
   for (int i = 0; i < d / 2; ++i) {
-    rot->turns[i] = std::pow(theta, -2.0 * i / d) / two_pi;
     if (pair_axis) {
       if (pair_axis[i] >= n_axes)
         return report_error(ATF_ERR_INVALID_ARG, "%s: pair_axis[%d] = %d, but there are %d axes", who, i,
@@ -258,7 +267,7 @@ atf_status atf_paged_decode(const atf_paged_decode_args* a, void* stream) {
   p.max_pages = a->max_pages;
   p.num_pages = static_cast<int>(a->num_pages);
   p.n_sel = a->selected ? a->n_select : 0;
-  method_windows(a->d, a->theta, a->alpha, &p.win, nullptr);
+  method_windows(a->d, a->theta, a->alpha, &p.win);
   // keys (64 elements: a chunk of four slots, group of four slots, chunk, page and
   // head): a box is the chunks of up to a tile's slots; values (64 elements, slot,
   // half of the row, page and head): a box is as many rows, half by half; both with
@@ -328,7 +337,7 @@ atf_status atf_page_select(const atf_page_select_args* a, void* stream) {
   p.n_sel = a->n_select;
   p.n_first = a->n_first;
   p.n_last = a->n_last;
-  method_windows(a->d, a->theta, a->alpha, &p.win, nullptr);
+  method_windows(a->d, a->theta, a->alpha, &p.win);
   cudaError_t e = launch_page_select(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATF_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
   return ATF_OK;

@@ -134,6 +134,18 @@ def test_bindings_refuse_wrong_tensors():
         atf.qk_norm_rope(q, q[:, :4], 1e4, torch.zeros(1, 2, dtype=torch.int32))
     with pytest.raises(TypeError):
         atf.qk_norm_rope(q, q[:, :4], 1e4, torch.zeros(2, 2, dtype=torch.int64), pair_axis=[0] * 63)
+    pos = torch.zeros(2, 2, dtype=torch.int64)
+    for axis, match in (([0] * 63 + [300], "300"), ([0] * 63 + ["x"], "int"), (5, "sequence")):
+        with pytest.raises(TypeError, match=match):
+            atf.qk_norm_rope(q, q[:, :4], 1e4, pos, pair_axis=axis)
+    with pytest.raises(TypeError, match="workspace"):
+        atf.paged_decode(q, kp, vp, table, lens, 1e4, 1.0, workspace=ws[::2])
+    with pytest.raises(TypeError, match="n_select"):
+        atf.page_select(q, torch.zeros(8, 4, 2, 128, dtype=torch.bfloat16), table, lens, 16, 1 << 40, 1e4, 1.0)
+    with pytest.raises(TypeError, match="a tensor is expected"):
+        atf.paged_decode(q, kp, vp, table, [1, 2], 1e4, 1.0)
+    with pytest.raises(TypeError, match="CUDA device"):
+        atf.qk_norm_rope(q, q[:, :4], 1e4, pos[:1])
     with pytest.raises(TypeError):
         atf.page_select(q, torch.zeros(8, 4, 2, 64, dtype=torch.bfloat16), table, lens, 16, 4, 1e4, 1.0)
 
