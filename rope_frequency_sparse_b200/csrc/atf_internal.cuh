@@ -143,6 +143,23 @@ constexpr unsigned int kErrBadLength = kErrBadData | 2;  // more keys than the p
 constexpr unsigned int kErrBadRows = kErrBadData | 3;    // row offsets outside the input
 constexpr unsigned int kErrBadSelect = kErrBadData | 4;  // selected page behind the sequence
 
+// A launch that may start while the stream's previous kernel drains; the kernel
+// calls pdl_wait() in every thread before it reads or writes what others write.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   }
   if (tid == kPdConsumers * 32) prefetch_tmap(&tm_k), prefetch_tmap(&tm_v);
   for (int i = tid; i < kMaxPairs; i += kPdThreads) sh->w[i] = p.win.w[i];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch_dependents();
+  pdl_wait();
 
   // ---- where this CTA's piece of the tile list begins
   const int per = (p.batch + kPdThreads - 1) / kPdThreads;  // sequences a thread sums
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(2 * D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
   __shared__ float s_f[kPagedCtas], s_red[2 * D / 32], s_acc[D], s_sum[2 * D / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   const int4 meta = p.meta[blockIdx.x];
   if (meta.x < 0) return;
   const int G = p.hq / p.hkv, g = blockIdx.y, tid = threadIdx.x;
@@ -671,19 +672,9 @@ static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, 
     if (e != cudaSuccess) return e;
     if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
-  kern<<<kPagedCtas, kPdThreads, bytes, s>>>(tk, tv, p);
-  e = cudaGetLastError();
+  e = launch_pdl(kern, kPagedCtas, kPdThreads, bytes, s, tk, tv, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPagedCtas, p.hq / p.hkv);
-  cfg.blockDim = dim3(2 * D);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
+  return launch_pdl(paged_combine_kernel<D>, dim3(kPagedCtas, p.hq / p.hkv), 2 * D, 0, s, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {

@@ -411,6 +411,32 @@ def test_select_ties_go_to_the_lowest_index():
     assert sel[0, 0].tolist() == list(range(1199)) + [2999]
 
 
+@pytest.mark.parametrize("pages,n_sel,scale", [(40, 9, 1.0), (200, 31, 1.0), (3000, 500, 1.0), (20000, 40, 1.0),
+                                               (300, 20, 1e30), (300, 20, 1e-25)])
+def test_select_orders_scores_that_32_bits_cannot_part(pages, n_sel, scale):
+    """Pages alike but for one dim whose share of the score is below 2^-30; sums beyond the range of 32 bits."""
+    Hkv, d, page = 2, 128, 16
+    bd = torch.sort(_normal(88, 1, Hkv, 2, d), dim=2).values.repeat(pages, 1, 1, 1)
+    bd[:, :, 1, 5] = _normal(89, pages, Hkv).abs()  # few distinct values: ties among them
+    bd[:, :, 0, 5] = 0
+    q = _normal(90, 1, 6, d)
+    q[..., 5] = 2.0 ** -30
+    bd, q = (bd.double() * scale).to(BF16), (q.double() * scale).to(BF16)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(3))[None].to(torch.int32).cuda()
+    sel = atf.page_select(q, bd, table, _int32([pages * page]), page, n_sel, 1e4, math.inf, 1, 1)
+    atf.atf_check()
+    want = paged.select(paged.f64(q), paged.f64(bd), table.cpu().numpy(), [pages * page], page, n_sel, 1e4, math.inf, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), want)
+
+
+def test_select_with_a_query_of_zeros_keeps_the_first_pages():
+    bd = torch.sort(_normal(97, 700, 1, 2, 64), dim=2).values
+    table = torch.arange(700, dtype=torch.int32, device="cuda")[None]
+    sel = atf.page_select(torch.zeros(1, 3, 64, dtype=BF16, device="cuda"), bd, table, _int32([700 * 32]), 32, 50, 1e4, 1.0)
+    atf.atf_check()
+    assert sel.flatten().tolist() == list(range(49)) + [699]
+
+
 def test_select_zeros_of_both_signs_are_equal():
     """A score of -0 (no pair counts, or products that are -0) ranks as +0."""
     bd = torch.zeros(2, 1, 2, 64, dtype=BF16, device="cuda")
