@@ -27,10 +27,10 @@
 // its passes over the scores: the order-preserving bit patterns are binned linearly
 // between the least and the greatest, and the bin of the last kept one again, until
 // few are left; a bin's edges are exact, so any distribution ends (each round parts
-// the least from the greatest).  The kept indices are emitted in order, a segment a warp.
+// the least from the greatest).  Where the places are at most a quarter of the groups
+// of 16 pages, groups are searched by their highest scores first, and pages only in
+// those that can hold a kept one: one SM's passes over 16384 scores took 12 us.
 #include <cuda_bf16.h>
-
-#include <atomic>
 
 #include "atf_internal.cuh"
 #include "ptx.cuh"
@@ -42,10 +42,12 @@ namespace {
 using u64 = unsigned long long;
 
 constexpr int kScoreThreads = 128;
+constexpr int kSelectThreads = 512;  // at most
 constexpr int kBins = 2048, kBinBits = 11;
 constexpr int kAgain = 256;       // pages that are scored again and ranked one against another
+constexpr int kCandidates = 1024;  // pages that are looked at one by one, of groups with a high score
 constexpr int kFewPages = 24;     // a bin of at most this many is not binned again: each goes to a warp
-constexpr int kHeldKeys = 16384;  // scores that are kept in shared memory
+constexpr int kHeld = 4;          // scores that a thread holds in registers at most
 // A step of 16 products is off by at most 18 * 2^-23 of the magnitudes summed so
 // far; 16 steps stay below 2^-14.8, and the rest of 2^-14 covers the roundings of S
 // and of the thresholds.
@@ -88,6 +90,18 @@ __device__ __forceinline__ int pool_page(const PageSelectParams& p, int entry) {
   return -1;
 }
 
+// What the first kernel leaves of a list of two pages or more in its max_pages 64-bit
+// words of workspace: the pages' scores, sortable, and of each group of 16 pages the
+// bits of the greatest S and the highest score that competes for a place (0: none).
+constexpr int kGroup = 16;
+struct Scores {
+  unsigned *key, *size, *high;
+  __device__ Scores(const PageSelectParams& p, int list)
+      : key(reinterpret_cast<unsigned*>(p.keys + static_cast<long long>(list) * p.max_pages)),
+        size(key + p.max_pages),
+        high(size + (p.max_pages + kGroup - 1) / kGroup) {}
+};
+
 }  // namespace
 
 // Scores of 16 pages a warp.  Lane (row, kcol) holds, of pages `row` and `row` + 8,
@@ -104,7 +118,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
   pdl_wait();
   const int len = select_len(p, b), ps = 1 << p.page_log2;
   const int pages = (len + ps - 1) >> p.page_log2;
-  if (static_cast<long long>(blockIdx.x) * (kScoreThreads / 2) >= pages) return;
+  if (pages <= p.n_sel || static_cast<long long>(blockIdx.x) * (kScoreThreads / 2) >= pages) return;
   __syncthreads();
   const int pg0 = blockIdx.x * (kScoreThreads / 2) + (tid >> 5) * 16 + row;
   const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
@@ -158,9 +172,12 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
       mma_bf16_16816(m, fa, y[2 * h] & kAbs, y[2 * h + 1] & kAbs);
     }
   }
+  Scores out(p, b * p.hkv + hk);
+  float size = 0.f;   // greatest S of the warp's pages
+  unsigned high = 0;  // and greatest score of those that compete for a place
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    float best = -INFINITY, size = 0.f;  // of query heads 2 kcol, 2 kcol + 1
+    float best = -INFINITY;  // of query heads 2 kcol, 2 kcol + 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * kcol + e >= G) continue;
@@ -168,14 +185,14 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
       size = m[2 * r + e] < INFINITY ? fmaxf(size, m[2 * r + e]) : INFINITY;  // NaN: infinite
     }
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
-      size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, off));
-    }
-    if (kcol == 0 && pg0 + 8 * r < pages)
-      p.keys[(static_cast<long long>(b) * p.hkv + hk) * p.max_pages + pg0 + 8 * r] =
-          static_cast<u64>(sortable(best)) << 32 | __float_as_uint(size);
+    for (int off = 1; off < 4; off <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
+    const int pg = pg0 + 8 * r;
+    if (kcol == 0 && pg < pages) out.key[pg] = sortable(best);
+    if (pg >= p.n_first && pg < pages - p.n_last) high = max(high, sortable(best));
   }
+  const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(size));  // in the order of magnitudes
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0 && pg0 < pages) out.size[pg0 / kGroup] = bits, out.high[pg0 / kGroup] = high;
 }
 
 namespace {
@@ -188,32 +205,36 @@ struct SelectShared {
   u64 lo, hi, cut;
   int need, count, n, above;
   int again[kAgain];
+  unsigned char mark[kAgain];
   unsigned least[32], greatest[32], size[32];
+  unsigned key[kCandidates];
+  int page[kCandidates];
+  int groups[kCandidates / kGroup], n_groups, n_kept;
+  int w[kMaxPairs];
 };
 
-// Narrows [lo, hi], which holds the need-th highest of the keys get(i), i0 <= i < i1,
-// until it is one key, or all of its `count` keys are needed, or they are at most
-// `few`.  On return `need` counts within [lo, hi].
-template <typename K, typename Get>
-__device__ __forceinline__ void narrow(SelectShared* sh, Get get, int i0, int i1, K& lo, K& hi, int& need, int& count,
-                                       int few) {
+// Narrows [lo, hi], which holds the need-th highest of the keys that each(f) calls
+// f(i, key, j) for, until it is one key, or all of its `count` keys are needed, or they
+// are at most `few`.  On return `need` counts within [lo, hi].
+template <typename K, typename Each>
+__device__ __forceinline__ void narrow(SelectShared* sh, Each each, K& lo, K& hi, int& need, int& count, int few) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
   while (lo < hi && count > few && count != need) {
     const int shift = max(0, static_cast<int>(sizeof(K)) * 8 - leading_zeros(hi - lo) - kBinBits);
     for (int i = tid; i < kBins; i += T) sh->hist[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = i0 + tid; i < i1; i += T) {
-      const K k = get(i);
+    each([&](int, K k, int) {
       if (k >= lo && k <= hi) atomicAdd(&sh->hist[static_cast<int>((k - lo) >> shift)], 1);
-    }
+    });
     __syncthreads();
     // the bin of the need-th, counted from the top: eight bins a thread
-    int sum = 0, incl = 0;
+    int n[8], sum = 0, incl = 0;
     const int top = kBins - 1 - 8 * tid;
     if (tid < kBins / 8) {
+      const int4 x = *reinterpret_cast<const int4*>(&sh->hist[top - 3]), y = *reinterpret_cast<const int4*>(&sh->hist[top - 7]);
+      n[0] = x.w, n[1] = x.z, n[2] = x.y, n[3] = x.x, n[4] = y.w, n[5] = y.z, n[6] = y.y, n[7] = y.x;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += sh->hist[top - j];
+      for (int j = 0; j < 8; ++j) sum += n[j];
       incl = sum;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -227,14 +248,16 @@ __device__ __forceinline__ void narrow(SelectShared* sh, Get get, int i0, int i1
       int before = incl - sum;
       for (int w = 0; w < warp; ++w) before += sh->warp_n[0][w];
       if (before < need && need <= before + sum) {
-        int bin = top;
-        while (before + sh->hist[bin] < need) before += sh->hist[bin--];
+        int bin = top, in = n[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+          if (before + in < need) before += in, bin = top - j, in = n[j];
         const K edge = lo + (static_cast<K>(bin) << shift);
         const K span = (static_cast<K>(1) << shift) - 1;
         sh->lo = edge;
         sh->hi = hi - edge < span ? hi : edge + span;
         sh->need = need - before;
-        sh->count = sh->hist[bin];
+        sh->count = in;
       }
     }
     __syncthreads();
@@ -267,26 +290,37 @@ __device__ __forceinline__ void block_range(SelectShared* sh, u64& lo, u64& hi) 
   }
 }
 
-// Writes, in order, the pages i for which kept(i) is set, and the first `ties` for
-// which tie(i) is; a segment of the pages a warp.
+// This thread's pages: 32 j + lane of its warp's segment of the list.  The scores of
+// up to kMine of them are held in registers.
+struct Mine {
+  int first, rounds;  // of the warp: every lane makes the same rounds
+  __device__ Mine(int pages) {
+    const int warps = blockDim.x >> 5;
+    rounds = ((pages + warps - 1) / warps + 31) >> 5;
+    first = static_cast<int>(threadIdx.x >> 5) * rounds * 32 + (threadIdx.x & 31);
+  }
+};
+
+// Writes, in order, the pages for which kept(i) is set, and the first `ties` for which
+// tie(i) is.
 template <typename Kept, typename Tie>
-__device__ __forceinline__ void emit(SelectShared* sh, int pages, int ties, int* out, Kept kept, Tie tie) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int seg = ((pages + warps - 1) / warps + 31) & ~31;
-  const int b0 = min(pages, warp * seg), b1 = min(pages, b0 + seg);
+__device__ __forceinline__ void emit(SelectShared* sh, const Mine& mine, int pages, int ties, int* out, Kept kept, Tie tie) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned below = (1u << lane) - 1;
   int a = 0, t = 0;
-  for (int i = b0 + lane; i - lane < b1; i += 32) {
-    a += __popc(__ballot_sync(0xffffffffu, i < b1 && kept(i)));
-    t += __popc(__ballot_sync(0xffffffffu, i < b1 && tie(i)));
+  for (int j = 0; j < mine.rounds; ++j) {
+    const int i = mine.first + 32 * j;
+    a += __popc(__ballot_sync(0xffffffffu, i < pages && kept(i)));
+    t += __popc(__ballot_sync(0xffffffffu, i < pages && tie(i)));
   }
   __syncthreads();  // the search still reads these
   if (lane == 0) sh->warp_n[0][warp] = a, sh->warp_n[1][warp] = t;
   __syncthreads();
-  a = t = 0;
-  for (int w = 0; w < warp; ++w) a += sh->warp_n[0][w], t += sh->warp_n[1][w];
-  const unsigned below = (1u << lane) - 1;
-  for (int i = b0 + lane; i - lane < b1; i += 32) {
-    const bool k = i < b1 && kept(i), e = i < b1 && tie(i);
+  a = __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_n[0][lane] : 0);
+  t = __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_n[1][lane] : 0);
+  for (int j = 0; j < mine.rounds; ++j) {
+    const int i = mine.first + 32 * j;
+    const bool k = i < pages && kept(i), e = i < pages && tie(i);
     const unsigned ma = __ballot_sync(0xffffffffu, k), mt = __ballot_sync(0xffffffffu, e);
     const int ai = a + __popc(ma & below), ti = t + __popc(mt & below);
     if (k || (e && ti < ties)) out[ai + min(ti, ties)] = i;
@@ -295,53 +329,89 @@ __device__ __forceinline__ void emit(SelectShared* sh, int pages, int ties, int*
   }
 }
 
-// The 64-bit score of a page, by a warp; one order of sums for every page.
-__device__ __forceinline__ u64 exact_score(const PageSelectParams& p, int b, int hk, int len, int page) {
-  const int lane = threadIdx.x & 31, G = p.hq / p.hkv, d = p.d;
+// The 64-bit score of a page, by a warp: four lanes a query head, each d/4 elements.
+// One order of sums for every page.
+template <int D>
+__device__ __forceinline__ u64 exact_score(const PageSelectParams& p, const int* windows, int b, int hk, int len, int page) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, G = p.hq / p.hkv;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const int entry = pool_page(p, p.page_table[static_cast<long long>(b) * p.max_pages + page]);
   const int near = page_distance(p, len, page);
-  const uint32_t* bounds = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.bounds) +
-                                                             (static_cast<long long>(max(entry, 0)) * p.hkv + hk) * 2 * d);
-  uint32_t mn[2] = {0u, 0u}, mx[2] = {0u, 0u};
-  for (int r = 0; r < d / 64; ++r) {
-    const int pair = 32 * r + lane;
-    if (entry >= 0 && near <= p.win.w[pair]) mn[r] = bounds[pair], mx[r] = bounds[d / 2 + pair];
-  }
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
-                                                        static_cast<long long>(hk) * G * d);
-  double best = -INFINITY;
-  for (int g = 0; g < G; ++g) {
-    double s = 0.0;
-    for (int r = 0; r < d / 64; ++r) {
-      const uint32_t w = q[g * (d / 2) + 32 * r + lane];
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
+                                                  (static_cast<long long>(hk) * G + min(g, G - 1)) * D);
+  const uint4* bounds = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) +
+                                                       (static_cast<long long>(max(entry, 0)) * p.hkv + hk) * 2 * D);
+  // a rolled loop, a piece ahead: this runs for a few pages a launch, and the fetch of
+  // straight-line code took longer than its execution
+  uint4 x = q[c], mn = entry >= 0 ? bounds[c] : zero, mx = entry >= 0 ? bounds[D / 8 + c] : zero;
+  double s = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < D / 32; ++j) {
+    const int next = 4 * min(j + 1, D / 32 - 1) + c;
+    const uint4 x1 = q[next], mn1 = entry >= 0 ? bounds[next] : zero, mx1 = entry >= 0 ? bounds[D / 8 + next] : zero;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+      const uint32_t l = k == 0 ? mn.x : k == 1 ? mn.y : k == 2 ? mn.z : mn.w;
+      const uint32_t h = k == 0 ? mx.x : k == 1 ? mx.y : k == 2 ? mx.z : mx.w;
+      const bool on = near <= windows[16 * j + 4 * c + k];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float x = e ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
-        const float l = e ? bf16hi_to_f32(mn[r]) : bf16lo_to_f32(mn[r]), h = e ? bf16hi_to_f32(mx[r]) : bf16lo_to_f32(mx[r]);
-        s += fmax(static_cast<double>(x) * l, static_cast<double>(x) * h);
+        const double y = e ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
+        const double best = fmax(y * (e ? bf16hi_to_f32(l) : bf16lo_to_f32(l)), y * (e ? bf16hi_to_f32(h) : bf16lo_to_f32(h)));
+        if (on) s += best;
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    best = fmax(best, s);
+    x = x1, mn = mn1, mx = mx1;
   }
-  return sortable(best);
+#pragma unroll
+  for (int off = 1; off < 4; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) s = fmax(s, __shfl_xor_sync(0xffffffffu, s, off));
+  return sortable(s);
+}
+
+// Of the `close` pages in sh->again marks the `need` best by 64-bit scores, equal ones
+// by lower index.
+template <int D>
+__device__ __forceinline__ void mark_best(SelectShared* sh, const PageSelectParams& p, int b, int hk, int len, int close,
+                                          int need) {
+  const int tid = threadIdx.x;
+  if (close > need) {
+    for (int i = tid >> 5; i < close; i += blockDim.x >> 5) {
+      const u64 x = exact_score<D>(p, sh->w, b, hk, len, sh->again[i]);
+      if ((tid & 31) == 0) sh->cand[i] = x;
+    }
+    __syncthreads();
+  }
+  if (tid < close) {
+    int before = 0;
+    if (close > need)
+      for (int j = 0; j < close; ++j)
+        before += sh->cand[j] > sh->cand[tid] || (sh->cand[j] == sh->cand[tid] && sh->again[j] < sh->again[tid]);
+    sh->mark[tid] = before < need;
+  }
+  __syncthreads();
 }
 
 }  // namespace
 
-// Threads: a multiple of 32, 256 to 1024.
-__global__ void __launch_bounds__(1024) page_select_kernel(const __grid_constant__ PageSelectParams p, int held) {
-  extern __shared__ unsigned s_keys[];  // `held` scores
-  __shared__ SelectShared s;
+// kMine: scores that a thread holds in registers; 0: more pages than that, the
+// scores are read again from memory by each pass.  Threads: a multiple of 32, 256
+// to kSelectThreads.
+template <int D, int kMine>
+__global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ PageSelectParams p) {
+  __shared__ __align__(16) SelectShared s;
   SelectShared* sh = &s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
   const int hk = blockIdx.x % p.hkv, b = blockIdx.x / p.hkv;
+  for (int i = tid; i < kMaxPairs; i += T) sh->w[i] = p.win.w[i];  // read after many barriers
   pdl_launch_dependents();
   pdl_wait();
   const int len = select_len(p, b);
   const int pages = (len + (1 << p.page_log2) - 1) >> p.page_log2;
-  u64* keys = p.keys + (static_cast<long long>(b) * p.hkv + hk) * p.max_pages;
+  u64* keys = p.keys + static_cast<long long>(blockIdx.x) * p.max_pages;  // 64-bit scores, where they are needed
+  const Scores scores(p, blockIdx.x);
   int* out = p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel;
   if (pages <= p.n_sel) {
     for (int i = tid; i < p.n_sel; i += T) out[i] = i < pages ? i : -1;
@@ -349,49 +419,162 @@ __global__ void __launch_bounds__(1024) page_select_kernel(const __grid_constant
   }
   // pages [i0, i1) compete for `places`
   const int i0 = p.n_first, i1 = pages - p.n_last, places = p.n_sel - p.n_first - p.n_last;
+  const Mine mine(pages);
   auto forced = [&](int i) { return i < i0 || i >= i1; };
   auto never = [](int) { return false; };
-  if (places == 0) return emit(sh, pages, 0, out, forced, never);
+  if (places == 0) return emit(sh, mine, pages, 0, out, forced, never);
 
-  const bool hold = pages <= held;
   unsigned lo = ~0u, hi = 0u, size = 0u;
-#pragma unroll 4
-  for (int i = i0 + tid; i < i1; i += T) {
-    const u64 x = keys[i];
-    const unsigned k = static_cast<unsigned>(x >> 32);
-    if (hold) s_keys[i] = k;
-    lo = min(lo, k);
-    hi = max(hi, k);
-    size = max(size, static_cast<unsigned>(x));  // magnitudes: their bits are in their order
-  }
-  if (tid == 0) sh->n = sh->above = 0;
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  size = __reduce_max_sync(0xffffffffu, size);
-  if (lane == 0) sh->least[warp] = lo, sh->greatest[warp] = hi, sh->size[warp] = size;
-  __syncthreads();
-  const int w = min(lane, warps - 1);
-  lo = __reduce_min_sync(0xffffffffu, sh->least[w]);
-  hi = __reduce_max_sync(0xffffffffu, sh->greatest[w]);
-  size = __reduce_max_sync(0xffffffffu, sh->size[w]);
+  const int groups = (pages + kGroup - 1) / kGroup;
+  auto range = [&]() {  // of the block, and the greatest S; sh->n and sh->above are cleared
+    if (tid == 0) sh->n = sh->above = sh->n_groups = sh->n_kept = 0;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    size = __reduce_max_sync(0xffffffffu, size);
+    if (lane == 0) sh->least[warp] = lo, sh->greatest[warp] = hi, sh->size[warp] = size;
+    __syncthreads();
+    const int w = min(lane, warps - 1);
+    lo = __reduce_min_sync(0xffffffffu, sh->least[w]);
+    hi = __reduce_max_sync(0xffffffffu, sh->greatest[w]);
+    size = __reduce_max_sync(0xffffffffu, sh->size[w]);
+  };
   // twice the largest error of a score; the constant covers products that vanish in fp32
-  const float slack = 2.f * (kEps * __uint_as_float(size) + 1e-30f);
-  auto approx = [&](int i) { return hold ? s_keys[i] : static_cast<unsigned>(keys[i] >> 32); };
+  auto slack_of = [](unsigned size) { return 2.f * (kEps * __uint_as_float(size) + 1e-30f); };
+  auto below = [](unsigned k, float by) { return sortable(from_sortable(k) - by); };
+
+  // ---- few places in a long list: only groups whose highest score is among the
+  // `places` highest of the groups, or close below, hold a kept page
+  if (groups >= 4 * places) {
+    auto each_group = [&](auto f) {
+#pragma unroll 4
+      for (int i = tid; i < groups; i += T) f(i, scores.high[i], 0);
+    };
+#pragma unroll 4
+    for (int i = tid; i < groups; i += T) {
+      const unsigned k = scores.high[i];
+      if (k) lo = min(lo, k);
+      hi = max(hi, k);
+      size = max(size, scores.size[i]);
+    }
+    range();
+    const float slack = slack_of(size);
+    if (slack < INFINITY) {
+      const unsigned top = hi;
+      int need = places, count = groups;
+      narrow(sh, each_group, lo, hi, need, count, kFewPages);
+      const unsigned least = below(lo, slack);
+      each_group([&](int i, unsigned k, int) {
+        if (k < least) return;
+        const int at = atomicAdd(&sh->n_groups, 1);
+        if (at < kCandidates / kGroup) sh->groups[at] = i;
+      });
+      __syncthreads();
+      const int n = sh->n_groups;
+      if (n <= kCandidates / kGroup) {
+        for (int x = tid; x < n * kGroup; x += T) {
+          const int i = sh->groups[x / kGroup] * kGroup + x % kGroup;
+          const unsigned k = i < pages && !forced(i) ? scores.key[i] : 0;
+          if (k < least) continue;
+          const int at = atomicAdd(&sh->n, 1);
+          sh->key[at] = k;
+          sh->page[at] = i;
+        }
+        __syncthreads();
+        const int m = sh->n;
+        auto each_candidate = [&](auto f) {
+          for (int x = tid; x < m; x += T) f(x, sh->key[x], 0);
+        };
+        lo = least, need = places, count = m;
+        hi = top;
+        narrow(sh, each_candidate, lo, hi, need, count, kFewPages);
+        const unsigned cut_lo = below(lo, slack), cut_hi = below(hi, -slack);
+        __syncthreads();
+        if (tid == 0) sh->n = 0;
+        __syncthreads();
+        for (int x = tid; x < m; x += T) {
+          const unsigned k = sh->key[x];
+          if (k > cut_hi) {
+            atomicAdd(&sh->above, 1);
+          } else if (k >= cut_lo) {
+            const int at = atomicAdd(&sh->n, 1);
+            if (at < kAgain) sh->again[at] = sh->page[x];
+          }
+        }
+        __syncthreads();
+        const int close = sh->n;
+        if (close <= kAgain) {
+          mark_best<D>(sh, p, b, hk, len, close, places - sh->above);
+          // the kept candidates by index, between the forced pages
+          for (int x = tid; x < m; x += T) {
+            const unsigned k = sh->key[x];
+            bool keep = k > cut_hi;
+            if (!keep && k >= cut_lo) {
+              int at = 0;
+              while (sh->again[at] != sh->page[x]) ++at;
+              keep = sh->mark[at];
+            }
+            if (keep) sh->hist[atomicAdd(&sh->n_kept, 1)] = sh->page[x];
+          }
+          __syncthreads();
+          for (int x = tid; x < p.n_sel; x += T) {
+            if (x < i0) {
+              out[x] = x;
+            } else if (x >= i0 + places) {
+              out[x] = pages - p.n_sel + x;
+            } else {
+              const int i = sh->hist[x - i0];
+              int before = 0;
+              for (int y = 0; y < places; ++y) before += sh->hist[y] < i;
+              out[i0 + before] = i;
+            }
+          }
+          return;
+        }
+      }
+    }
+    __syncthreads();
+    lo = ~0u, hi = 0u;
+  }
+
+  // ---- every page
+  unsigned mk[kMine ? kMine : 1];
+  for (int i = tid; i < groups; i += T) size = max(size, scores.size[i]);
+  if constexpr (kMine > 0) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) mk[j] = scores.key[min(mine.first + 32 * j, pages - 1)];  // all under way at once
+  }
+  auto each = [&](auto f) {
+    if constexpr (kMine > 0) {
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int i = mine.first + 32 * j;
+        if (j < mine.rounds && !forced(i)) f(i, mk[j], j);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = i0 + tid; i < i1; i += T) f(i, scores.key[i], 0);
+    }
+  };
+  each([&](int, unsigned k, int) { lo = min(lo, k), hi = max(hi, k); });
+  range();
+  const float slack = slack_of(size);
   bool again = !(slack < INFINITY);
   if (!again) {
     int need = places, count = i1 - i0;
-    narrow(sh, approx, i0, i1, lo, hi, need, count, kFewPages);
-    const unsigned cut_lo = sortable(from_sortable(lo) - slack), cut_hi = sortable(from_sortable(hi) + slack);
+    narrow(sh, each, lo, hi, need, count, kFewPages);
+    const unsigned cut_lo = below(lo, slack), cut_hi = below(hi, -slack);
     int above = 0;
-#pragma unroll 4
-    for (int i = i0 + tid; i < i1; i += T) {
-      const unsigned k = approx(i);
-      above += k > cut_hi;
-      if (k >= cut_lo && k <= cut_hi) {
+    unsigned bits = 0, unsure = 0;  // this thread's pages that are kept, and that are scored again
+    each([&](int i, unsigned k, int j) {
+      if (k > cut_hi) {
+        ++above;
+        bits |= 1u << j;
+      } else if (k >= cut_lo) {
+        unsure |= 1u << j;
         const int at = atomicAdd(&sh->n, 1);
         if (at < kAgain) sh->again[at] = i;
       }
-    }
+    });
     above = __reduce_add_sync(0xffffffffu, above);
     if (lane == 0) atomicAdd(&sh->above, above);
     __syncthreads();
@@ -399,42 +582,60 @@ __global__ void __launch_bounds__(1024) page_select_kernel(const __grid_constant
     need = places - sh->above;  // of the close ones
     again = close > kAgain;
     if (!again) {
-      if (close > need) {
-        for (int i = warp; i < close; i += warps) {
-          const u64 x = exact_score(p, b, hk, len, sh->again[i]);
-          if (lane == 0) sh->cand[i] = x;
+      mark_best<D>(sh, p, b, hk, len, close, need);
+      auto chosen = [&](int i) {
+        int at = 0;
+        while (sh->again[at] != i) ++at;
+        return sh->mark[at] != 0;
+      };
+      if constexpr (kMine > 0) {
+        for (; unsure; unsure &= unsure - 1) {
+          const int j = __ffs(unsure) - 1;
+          if (chosen(mine.first + 32 * j)) bits |= 1u << j;
         }
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          const int i = mine.first + 32 * j;
+          if (j < mine.rounds && i < pages && forced(i)) bits |= 1u << j;
+        }
+        const int n = __reduce_add_sync(0xffffffffu, __popc(bits));
+        if (lane == 0) sh->warp_n[1][warp] = n;
         __syncthreads();
+        int at = __reduce_add_sync(0xffffffffu, lane < warp ? sh->warp_n[1][lane] : 0);
+        if (!n) return;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          const unsigned m = __ballot_sync(0xffffffffu, bits >> j & 1);
+          if (bits >> j & 1) out[at + __popc(m & ((1u << lane) - 1))] = mine.first + 32 * j;
+          at += __popc(m);
+        }
+      } else {
+        auto kept = [&](int i) {
+          if (forced(i)) return true;
+          const unsigned k = scores.key[i];
+          return k > cut_hi || (k >= cut_lo && chosen(i));
+        };
+        emit(sh, mine, pages, 0, out, kept, never);
       }
-      if (tid < close) {
-        const int mine = sh->again[tid];
-        int before = 0;
-        if (close > need)
-          for (int j = 0; j < close; ++j)
-            before += sh->cand[j] > sh->cand[tid] || (sh->cand[j] == sh->cand[tid] && sh->again[j] < mine);
-        const unsigned mark = before < need ? ~0u : 0u;  // its score from here on
-        if (hold)
-          s_keys[mine] = mark;
-        else
-          keys[mine] = static_cast<u64>(mark) << 32;
-      }
-      __syncthreads();
-      return emit(sh, pages, 0, out, [&](int i) { return forced(i) || approx(i) > cut_hi; }, never);
+      return;
     }
   }
 
   // every score in 64 bits
   for (int i = i0 + warp; i < i1; i += warps) {
-    const u64 x = exact_score(p, b, hk, len, i);
+    const u64 x = exact_score<D>(p, sh->w, b, hk, len, i);
     if (lane == 0) keys[i] = x;
   }
   __syncthreads();
   if (tid == 0) sh->n = 0;
+  auto each64 = [&](auto f) {
+    for (int i = i0 + tid; i < i1; i += T) f(i, keys[i], 0);
+  };
   u64 lo64 = ~0ull, hi64 = 0;
-  for (int i = i0 + tid; i < i1; i += T) lo64 = min(lo64, keys[i]), hi64 = max(hi64, keys[i]);
+  each64([&](int, u64 k, int) { lo64 = min(lo64, k), hi64 = max(hi64, k); });
   block_range(sh, lo64, hi64);
   int need = places, count = i1 - i0;
-  narrow(sh, [&](int i) { return keys[i]; }, i0, i1, lo64, hi64, need, count, kAgain);
+  narrow(sh, each64, lo64, hi64, need, count, kAgain);
   // kept: every key above `cut`, and the first `ties` that equal it
   u64 cut = lo64;
   int ties = need;
@@ -442,20 +643,19 @@ __global__ void __launch_bounds__(1024) page_select_kernel(const __grid_constant
     cut = lo64 ? lo64 - 1 : 0;
     ties = lo64 ? 0 : count;
   } else if (lo64 < hi64) {
-    for (int i = i0 + tid; i < i1; i += T) {
-      const u64 k = keys[i];
+    each64([&](int, u64 k, int) {
       if (k >= lo64 && k <= hi64) sh->cand[atomicAdd(&sh->n, 1)] = k;
-    }
+    });
     __syncthreads();
     if (tid < count) {
-      const u64 mine = sh->cand[tid];
+      const u64 own = sh->cand[tid];
       int above = 0, equal = 0;
       for (int j = 0; j < count; ++j) {
-        above += sh->cand[j] > mine;
-        equal += sh->cand[j] == mine;
+        above += sh->cand[j] > own;
+        equal += sh->cand[j] == own;
       }
       if (above < need && need <= above + equal) {  // so do its equals, with the same values
-        sh->cut = mine;
+        sh->cut = own;
         sh->need = need - above;
       }
     }
@@ -463,27 +663,24 @@ __global__ void __launch_bounds__(1024) page_select_kernel(const __grid_constant
     cut = sh->cut;
     ties = sh->need;
   }
-  emit(sh, pages, ties, out, [&](int i) { return forced(i) || keys[i] > cut; },
+  emit(sh, mine, pages, ties, out, [&](int i) { return forced(i) || keys[i] > cut; },
        [&](int i) { return !forced(i) && keys[i] == cut; });
 }
 
-cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s) {
+template <int D>
+static cudaError_t launch_select(const PageSelectParams& p, cudaStream_t s) {
   const int per = kScoreThreads / 2;
   const dim3 grid((p.max_pages + per - 1) / per, p.batch * p.hkv);
-  cudaError_t e = launch_pdl(p.d == 64 ? page_score_kernel<64> : page_score_kernel<128>, grid, kScoreThreads, 0, s, p);
+  cudaError_t e = launch_pdl(page_score_kernel<D>, grid, kScoreThreads, 0, s, p);
   if (e != cudaSuccess) return e;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static std::atomic<u64> configured{0};  // one bit per device; setting it twice is harmless
-  if (dev >= 64 || !(configured.load(std::memory_order_acquire) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(page_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_acq_rel);
-  }
-  const int held = p.max_pages < kHeldKeys ? p.max_pages : kHeldKeys;
-  const int threads = p.max_pages <= 2048 ? 256 : 1024;
-  return launch_pdl(page_select_kernel, p.batch * p.hkv, threads, held * 4, s, p, held);
+  const int lists = p.batch * p.hkv;
+  if (p.max_pages > kSelectThreads * kHeld) return launch_pdl(page_select_kernel<D, 0>, lists, kSelectThreads, 0, s, p);
+  const int threads = p.max_pages <= 256 * kHeld ? 256 : (p.max_pages + 32 * kHeld - 1) / (32 * kHeld) * 32;
+  return launch_pdl(page_select_kernel<D, kHeld>, lists, threads, 0, s, p);
+}
+
+cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s) {
+  return p.d == 64 ? launch_select<64>(p, s) : launch_select<128>(p, s);
 }
 
 }  // namespace atf

@@ -386,6 +386,8 @@ def test_decode_of_a_cache_past_2_31_elements():
     ([1000, 16, 0, 333], 28, 4, 128, 16, 1e4, 1.0, 9, 1, 1), ([9000, 200], 4, 2, 64, 16, 1e4, math.inf, 40, 0, 0),
     ([129], 8, 1, 128, 128, 1e7, 1.0, 1, 0, 1), ([20000], 3, 1, 64, 16, 1e4, 0.5, 700, 3, 5),
     ([640, 641, 639], 7, 7, 128, 32, 1e4, 1.0, 20, 2, 2), ([5000], 8, 1, 128, 16, 1.0001, 0.1, 12, 0, 0),
+    ([50000, 4097, 33], 4, 2, 64, 16, 1e4, 1.0, 12, 1, 1), ([36000, 20000], 2, 2, 64, 16, 1e4, 0.5, 5, 0, 0),
+    ([16 * 16 * 40, 16 * 16 * 40 - 16], 2, 1, 64, 16, 1e4, math.inf, 13, 2, 1), ([32, 31], 4, 2, 64, 16, 1e4, 1.0, 1, 0, 0),
 ])
 def test_select_against_oracle(lens, Hq, Hkv, d, page, theta, alpha, n_sel, first, last):
     table, pool = _tables(lens, page, 81, extra=2)
