@@ -88,6 +88,7 @@ struct NormRopeParams {
   const void *q_weight, *k_weight;  // [d] in the element type, nullable: no norm
   const long long* pos;             // [n_axes][tokens]
   int tokens, hq, hkv, d, pairing, fp32;
+  bool wide;                        // the outputs are 32-byte aligned
   float eps;
   RotaryTable rot;
 };
@@ -101,6 +102,8 @@ struct PagedAppendParams {
   const int *page_table, *start, *cu;  // cu nullable: one token per sequence
   const long long* pos;             // nullable: the slot
   int tokens, batch, hq, hkv, d, pairing, page_log2, max_pages, num_pages;
+  long long items;                  // at least the pages that the new tokens of all sequences fall into
+  bool wide;                        // q_out and the pages are 32-byte aligned
   float eps;
   unsigned int* err;
   RotaryTable rot;
@@ -163,6 +166,7 @@ cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t sm
 // Launchers (return cudaGetLastError() of the launch).
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
+long long paged_append_blocks(const PagedAppendParams& p);  // CTAs of a ragged append
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 cudaStream_t s);
 cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s);

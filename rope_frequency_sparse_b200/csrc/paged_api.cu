@@ -15,6 +15,7 @@ using namespace atf;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Rows of a strided operand: a stride in elements that keeps every row 16-byte
@@ -146,6 +147,7 @@ atf_status atf_qk_norm_rope(const atf_qk_norm_rope_args* a, void* stream) {
   p.d = a->d;
   p.pairing = a->pairing;
   p.fp32 = a->dtype == ATF_FP32;
+  p.wide = aligned32(p.q_out) && aligned32(p.k_out);
   p.eps = a->eps;
   cudaError_t e = launch_qk_norm_rope(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATF_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
@@ -215,6 +217,11 @@ atf_status atf_paged_append(const atf_paged_append_args* a, void* stream) {
   p.page_log2 = page_log2(a->page_size);
   p.max_pages = a->max_pages;
   p.num_pages = static_cast<int>(a->num_pages);
+  // a sequence with n > 0 new tokens touches at most (n - 1) / page + 2 pages
+  p.items = (p.tokens >> p.page_log2) + 2LL * (p.batch < p.tokens ? p.batch : p.tokens);
+  p.wide = aligned32(p.q_out) && aligned32(p.k_pages) && aligned32(p.v_pages);
+  if (p.cu && paged_append_blocks(p) > 0x7fffffffLL)
+    return report_error(ATF_ERR_UNSUPPORTED, "%s: too many tokens, sequences and heads for one call", who);
   p.eps = a->eps;
   cudaError_t e = launch_paged_append(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATF_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));

@@ -6,14 +6,18 @@
 //   (y_a, y_b) of pair i turned by pos[axis(i)] * theta^(-2i/d)
 //
 // all in fp32 and rounded once.  The angle is reduced to a fraction of a turn in
-// fp64 (at position 2^20 an fp32 angle is off by more than a bf16 step), and the
-// sine and cosine of that fraction are fp32.
+// fp64 (at position 2^20 an fp32 angle is off by more than a bf16 step).  The sine
+// and cosine of that fraction are fp32's for fp32 rows; for bf16 rows the fast ones,
+// off by at most 2^-21 on [-pi, pi], 2^-13 of a bf16 half step.
 //
-// One thread owns a token's 8-pair chunk c: elements 16c..16c+15 of a head
-// (interleaved pairs) or 8c..8c+7 and d/2+8c..d/2+8c+7 (rotate-half), which are
-// the 16 outputs 16c..16c+15 either way and one 32-byte row of the key pages.  It
-// evaluates the chunk's eight angles once and loops over heads; the d/16 lanes of
-// a head add their squares by shuffles.
+// Bound by the rows' bytes, read once and written once.  One thread owns a token's
+// 8-pair chunk c: elements 16c..16c+15 of a head (interleaved pairs) or 8c..8c+7 and
+// d/2+8c..d/2+8c+7 (rotate-half), which are the 16 outputs 16c..16c+15 either way and
+// one 32-byte row of the key pages, written by one store.  It evaluates the chunk's
+// eight angles once for up to kRows heads, whose loads are all under way before the
+// first is used (one at a time: 32 us for 8192 tokens of 28 + 4 heads of 128, 20.5 at
+// the copy rate); the d/16 lanes of a head add their squares by shuffles.  Few rows
+// take one head a thread: there the latency of a thread's chain is what counts.
 #include <cuda_bf16.h>
 
 #include "atf_internal.cuh"
@@ -24,22 +28,35 @@ namespace atf {
 namespace {
 
 constexpr int kNrThreads = 128;
+constexpr int kRows = 4;  // heads of a thread where there are many
 
-template <typename T>
+// 32 bytes to dst: one store where `wide` (dst 32-byte aligned), else two.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <typename T, bool kHalf>
 struct Chunk;  // 16 elements as loaded: the first components a[8] and second b[8] of eight pairs
 
-template <>
-struct Chunk<__nv_bfloat16> {
+template <bool kHalf>
+struct Chunk<__nv_bfloat16, kHalf> {
   uint4 lo, hi;
-  __device__ void load(const __nv_bfloat16* row, int c, int d, bool half) {
-    lo = *reinterpret_cast<const uint4*>(row + (half ? 8 * c : 16 * c));
-    hi = *reinterpret_cast<const uint4*>(row + (half ? d / 2 + 8 * c : 16 * c + 8));
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int d) {
+    lo = *reinterpret_cast<const uint4*>(row + (kHalf ? 8 * c : 16 * c));
+    hi = *reinterpret_cast<const uint4*>(row + (kHalf ? d / 2 + 8 * c : 16 * c + 8));
   }
-  __device__ void pairs(bool half, float* a, float* b) const {
+  __device__ __forceinline__ void pairs(float* a, float* b) const {
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (half) {
+      if (kHalf) {
         a[k] = (k & 1) ? bf16hi_to_f32(w[k >> 1]) : bf16lo_to_f32(w[k >> 1]);
         b[k] = (k & 1) ? bf16hi_to_f32(w[4 + (k >> 1)]) : bf16lo_to_f32(w[4 + (k >> 1)]);
       } else {
@@ -48,36 +65,39 @@ struct Chunk<__nv_bfloat16> {
       }
     }
   }
-  __device__ static void store(__nv_bfloat16* dst, const float* a, const float* b) {
+  __device__ __forceinline__ static void store(__nv_bfloat16* dst, const float* a, const float* b, bool wide) {
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(a[k], b[k]);
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    store32(dst, w, wide);
   }
 };
 
-template <>
-struct Chunk<float> {
+template <bool kHalf>
+struct Chunk<float, kHalf> {
   float4 v[4];
-  __device__ void load(const float* row, int c, int d, bool half) {
-    const float4* lo = reinterpret_cast<const float4*>(row + (half ? 8 * c : 16 * c));
-    const float4* hi = reinterpret_cast<const float4*>(row + (half ? d / 2 + 8 * c : 16 * c + 8));
+  __device__ __forceinline__ void load(const float* row, int c, int d) {
+    const float4* lo = reinterpret_cast<const float4*>(row + (kHalf ? 8 * c : 16 * c));
+    const float4* hi = reinterpret_cast<const float4*>(row + (kHalf ? d / 2 + 8 * c : 16 * c + 8));
     v[0] = lo[0], v[1] = lo[1], v[2] = hi[0], v[3] = hi[1];
   }
-  __device__ void pairs(bool half, float* a, float* b) const {
+  __device__ __forceinline__ void pairs(float* a, float* b) const {
     const float w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                          v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      a[k] = half ? w[k] : w[2 * k];
-      b[k] = half ? w[8 + k] : w[2 * k + 1];
+      a[k] = kHalf ? w[k] : w[2 * k];
+      b[k] = kHalf ? w[8 + k] : w[2 * k + 1];
     }
   }
-  __device__ static void store(float* dst, const float* a, const float* b) {
+  __device__ __forceinline__ static void store(float* dst, const float* a, const float* b, bool wide) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      reinterpret_cast<float4*>(dst)[k] = make_float4(a[2 * k], b[2 * k], a[2 * k + 1], b[2 * k + 1]);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[2 * k] = __float_as_uint(a[4 * h + k]), w[2 * k + 1] = __float_as_uint(b[4 * h + k]);
+      store32(dst + 8 * h, w, wide);
+    }
   }
 };
 
@@ -86,7 +106,7 @@ struct RotaryShared {
   unsigned char axis[kMaxPairs];
 };
 
-__device__ void load_rotary(RotaryShared* sh, const RotaryTable& rot, int d) {
+__device__ __forceinline__ void load_rotary(RotaryShared* sh, const RotaryTable& rot, int d) {
   for (int i = threadIdx.x; i < d / 2; i += blockDim.x) {
     sh->turns[i] = rot.turns[i];
     sh->axis[i] = rot.axis[i];
@@ -94,18 +114,34 @@ __device__ void load_rotary(RotaryShared* sh, const RotaryTable& rot, int d) {
   __syncthreads();
 }
 
+// Positions of a token on up to kMaxAxes axes.
+struct Position {
+  double at[kMaxAxes];
+  __device__ __forceinline__ void load(const long long* pos, int n_axes, long long tokens, long long t) {
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) at[a] = a < n_axes ? static_cast<double>(pos[a * tokens + t]) : 0.0;
+  }
+};
+
 // Cosine and sine of the eight angles of chunk c.
-__device__ __forceinline__ void chunk_angles(const RotaryShared* sh, int c, const long long* pos, int n_axes, float* cs,
-                                             float* sn) {
+template <bool kFast>
+__device__ __forceinline__ void chunk_angles(const RotaryShared* sh, int c, const Position& pos, int n_axes, float* cs, float* sn) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    long long p = pos[0];
+    double p = pos.at[0];
     if (n_axes > 1) {
       const int a = sh->axis[8 * c + k];
-      p = a == 1 ? pos[1] : a == 2 ? pos[2] : a == 3 ? pos[3] : p;
+      p = a == 1 ? pos.at[1] : a == 2 ? pos.at[2] : a == 3 ? pos.at[3] : p;
     }
-    const double t = static_cast<double>(p) * sh->turns[8 * c + k];
-    sincospif(2.0f * static_cast<float>(t - rint(t)), &sn[k], &cs[k]);
+    const double t = p * sh->turns[8 * c + k];
+    const float turn = static_cast<float>(t - rint(t));
+    if (kFast) {
+      const float x = 6.283185307f * turn;
+      sn[k] = __sinf(x);
+      cs[k] = __cosf(x);
+    } else {
+      sincospif(2.0f * turn, &sn[k], &cs[k]);
+    }
   }
 }
 
@@ -135,116 +171,85 @@ __device__ __forceinline__ void norm_rotate(float* a, float* b, bool norm, const
   }
 }
 
+// A token's chunk of up to R neighbouring heads and their weights.
+template <typename T, int D, int R, bool kHalf>
+struct Rows {
+  Chunk<T, kHalf> in[R], weight;
+  __device__ __forceinline__ void load(const T* x, int n, int c, const T* w) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) in[r].load(x + (R == 1 ? 0 : min(r, n - 1)) * D, c, D);
+    if (w) weight.load(w, c, D);
+  }
+  // Heads r < n to out + r * d, where `live`; every lane of the warp calls it.
+  __device__ __forceinline__ void finish(T* out, int n, bool norm, float eps, const float* cs, const float* sn, bool live,
+                                         bool wide) const {
+    float wa[8], wb[8];
+    if (norm) weight.pairs(wa, wb);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float a[8], b[8];
+      in[r].pairs(a, b);
+      norm_rotate<D>(a, b, norm, wa, wb, eps, cs, sn);
+      if (live && r < n) Chunk<T, kHalf>::store(out + r * D, a, b, wide);
+    }
+  }
+};
+
 }  // namespace
 
-// Dense form.  Thread = (token, chunk), blockIdx.y = a group of kNrRows heads of
-// the queries and keys taken as one list.
-constexpr int kNrRows = 8;
-
-template <typename T, int D>
+// Dense form.  Thread = (token, chunk), blockIdx.y = R query heads or, behind them, R
+// key heads.
+template <typename T, int D, int R, bool kHalf>
 __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int NC = D / 16;
   __shared__ RotaryShared sh;
   load_rotary(&sh, p.rot, D);
+  pdl_launch_dependents();
+  pdl_wait();
   const long long idx = static_cast<long long>(blockIdx.x) * kNrThreads + threadIdx.x;
   const int c = static_cast<int>(idx % NC);
   const bool live = idx / NC < p.tokens;
   const long long t = live ? idx / NC : p.tokens - 1;
-  const bool half = p.pairing != 0;
-  long long pos[kMaxAxes];
-  for (int a = 0; a < kMaxAxes; ++a) pos[a] = a < p.rot.n_axes ? p.pos[static_cast<long long>(a) * p.tokens + t] : 0;
+  const int q_groups = (p.hq + R - 1) / R;
+  const bool key = static_cast<int>(blockIdx.y) >= q_groups;
+  const int heads = key ? p.hkv : p.hq, h = (key ? blockIdx.y - q_groups : blockIdx.y) * R, n = min(R, heads - h);
+  const T* w = static_cast<const T*>(key ? p.k_weight : p.q_weight);
+  Rows<T, D, R, kHalf> rows;
+  rows.load(static_cast<const T*>(key ? p.k : p.q) + t * (key ? p.k_stride : p.q_stride) + h * D, n, c, w);
+  Position pos;
+  pos.load(p.pos, p.rot.n_axes, p.tokens, t);
   float cs[8], sn[8];
-  chunk_angles(&sh, c, pos, p.rot.n_axes, cs, sn);
-  const int r1 = min(p.hq + p.hkv, (static_cast<int>(blockIdx.y) + 1) * kNrRows);
-  for (int r = blockIdx.y * kNrRows; r < r1; ++r) {
-    const bool key = r >= p.hq;
-    const int h = key ? r - p.hq : r;
-    const T* x = static_cast<const T*>(key ? p.k : p.q);
-    if (!x) continue;
-    const T* w = static_cast<const T*>(key ? p.k_weight : p.q_weight);
-    Chunk<T> ch;
-    ch.load(x + t * (key ? p.k_stride : p.q_stride) + h * D, c, D, half);
-    float a[8], b[8], wa[8], wb[8];
-    ch.pairs(half, a, b);
-    if (w) {
-      Chunk<T> cw;
-      cw.load(w, c, D, half);
-      cw.pairs(half, wa, wb);
-    }
-    norm_rotate<D>(a, b, w != nullptr, wa, wb, p.eps, cs, sn);
-    T* out = static_cast<T*>(key ? p.k_out : p.q_out);
-    if (live) Chunk<T>::store(out + (t * (key ? p.hkv : p.hq) + h) * D + 16 * c, a, b);
-  }
+  chunk_angles<sizeof(T) == 2>(&sh, c, pos, p.rot.n_axes, cs, sn);
+  rows.finish(static_cast<T*>(key ? p.k_out : p.q_out) + (t * heads + h) * D + 16 * c, n, w != nullptr, p.eps, cs, sn, live,
+              p.wide);
+}
+
+template <typename T, int D, bool kHalf>
+static cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s) {
+  const long long chunks = static_cast<long long>(p.tokens) * (D / 16);
+  const unsigned blocks = static_cast<unsigned>((chunks + kNrThreads - 1) / kNrThreads);
+  // kRows heads a thread once that still leaves every SM 512 threads
+  const bool many = chunks * (p.hq + p.hkv) >= 148LL * 512 * kRows;
+  if (!many) return launch_pdl(qk_norm_rope_kernel<T, D, 1, kHalf>, dim3(blocks, p.hq + p.hkv), kNrThreads, 0, s, p);
+  const int groups = (p.hq + kRows - 1) / kRows + (p.hkv + kRows - 1) / kRows;
+  return launch_pdl(qk_norm_rope_kernel<T, D, kRows, kHalf>, dim3(blocks, groups), kNrThreads, 0, s, p);
+}
+
+template <typename T, int D>
+static cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s) {
+  return p.pairing ? launch_norm_rope<T, D, true>(p, s) : launch_norm_rope<T, D, false>(p, s);
 }
 
 cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t s) {
-  const long long threads = static_cast<long long>(p.tokens) * (p.d / 16);
-  const dim3 grid(static_cast<unsigned>((threads + kNrThreads - 1) / kNrThreads), (p.hq + p.hkv + kNrRows - 1) / kNrRows);
-  if (p.fp32)
-    p.d == 64 ? qk_norm_rope_kernel<float, 64><<<grid, kNrThreads, 0, s>>>(p)
-              : qk_norm_rope_kernel<float, 128><<<grid, kNrThreads, 0, s>>>(p);
-  else
-    p.d == 64 ? qk_norm_rope_kernel<__nv_bfloat16, 64><<<grid, kNrThreads, 0, s>>>(p)
-              : qk_norm_rope_kernel<__nv_bfloat16, 128><<<grid, kNrThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.fp32) return p.d == 64 ? launch_norm_rope<float, 64>(p, s) : launch_norm_rope<float, 128>(p, s);
+  return p.d == 64 ? launch_norm_rope<__nv_bfloat16, 64>(p, s) : launch_norm_rope<__nv_bfloat16, 128>(p, s);
 }
 
 // ------------------------------------------------------------------ paged append
 
 namespace {
 
-// One new token's chunk of kv head kvh: its queries to q_out, its key and value
-// to slot `at` of page `page` (page < 0: nowhere).  Returns the rounded key in
-// kw.  Every lane of the warp calls it; `live` lanes write.
-template <int D>
-__device__ __forceinline__ void append_token(const PagedAppendParams& p, const RotaryShared* sh, long long row, long long slot,
-                                             int kvh, int c, int page, int at, bool live, uint32_t* kw) {
-  using T = __nv_bfloat16;
-  const bool half = p.pairing != 0;
-  const int G = p.hq / p.hkv;
-  Chunk<T> kc;
-  kc.load(static_cast<const T*>(p.k) + row * p.k_stride + kvh * D, c, D, half);
-  const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + row * p.v_stride + kvh * D + 16 * c);
-  const uint4 v0 = vr[0], v1 = vr[1];
-  long long pos[kMaxAxes] = {slot, 0, 0, 0};
-  if (p.pos)
-    for (int a = 0; a < p.rot.n_axes; ++a) pos[a] = p.pos[static_cast<long long>(a) * p.tokens + row];
-  float cs[8], sn[8], a[8], b[8], wa[8], wb[8];
-  chunk_angles(sh, c, pos, p.pos ? p.rot.n_axes : 1, cs, sn);
-  if (p.k_weight) {
-    Chunk<T> cw;
-    cw.load(static_cast<const T*>(p.k_weight), c, D, half);
-    cw.pairs(half, wa, wb);
-  }
-  kc.pairs(half, a, b);
-  norm_rotate<D>(a, b, p.k_weight != nullptr, wa, wb, p.eps, cs, sn);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) kw[k] = pack_bf16x2(a[k], b[k]);
-  if (live && page >= 0) {
-    const long long ps = 1LL << p.page_log2;
-    const long long head = static_cast<long long>(page) * p.hkv + kvh;
-    uint4* kd = reinterpret_cast<uint4*>(static_cast<T*>(p.k_pages) + ((head * (D / 16) + c) * ps + at) * 16);
-    kd[0] = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-    kd[1] = make_uint4(kw[4], kw[5], kw[6], kw[7]);
-    uint4* vd = reinterpret_cast<uint4*>(static_cast<T*>(p.v_pages) + (head * ps + at) * D + 16 * c);
-    vd[0] = v0;
-    vd[1] = v1;
-  }
-  if (!p.q) return;
-  if (p.q_weight) {
-    Chunk<T> cw;
-    cw.load(static_cast<const T*>(p.q_weight), c, D, half);
-    cw.pairs(half, wa, wb);
-  }
-  for (int g = 0; g < G; ++g) {
-    const int h = kvh * G + g;
-    Chunk<T> qc;
-    qc.load(static_cast<const T*>(p.q) + row * p.q_stride + h * D, c, D, half);
-    qc.pairs(half, a, b);
-    norm_rotate<D>(a, b, p.q_weight != nullptr, wa, wb, p.eps, cs, sn);
-    if (live) Chunk<T>::store(static_cast<T*>(p.q_out) + (row * p.hq + h) * D + 16 * c, a, b);
-  }
-}
+using bf16 = __nv_bfloat16;
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -272,122 +277,251 @@ __device__ __forceinline__ int page_of(const PagedAppendParams& p, int b, long l
   return page;
 }
 
-// Bounds rows of chunk c: 8 words of minima and of maxima.
+// A key's and a value's chunk to slot `at` of a page.
+template <int D>
+__device__ __forceinline__ void store_slot(const PagedAppendParams& p, int page, int kvh, int c, int at, const uint32_t* k,
+                                           const uint32_t* v) {
+  const long long ps = 1LL << p.page_log2, head = static_cast<long long>(page) * p.hkv + kvh;
+  store32(static_cast<bf16*>(p.k_pages) + ((head * (D / 16) + c) * ps + at) * 16, k, p.wide);
+  store32(static_cast<bf16*>(p.v_pages) + (head * ps + at) * D + 16 * c, v, p.wide);
+}
+
+// Bounds row of chunk c: 8 words of minima or maxima.
 template <int D>
 __device__ __forceinline__ uint4* bounds_row(const PagedAppendParams& p, int page, int kvh, int which, int c) {
-  return reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.bounds) +
-                                  ((static_cast<long long>(page) * p.hkv + kvh) * 2 + which) * D + 16 * c);
+  return reinterpret_cast<uint4*>(static_cast<bf16*>(p.bounds) + ((static_cast<long long>(page) * p.hkv + kvh) * 2 + which) * D +
+                                  16 * c);
+}
+
+__device__ __forceinline__ void load32(uint32_t* w, const bf16* x) {
+  const uint4 a = reinterpret_cast<const uint4*>(x)[0], b = reinterpret_cast<const uint4*>(x)[1];
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
 }  // namespace
 
-// One token per sequence: thread = (sequence, kv head, chunk).
-template <int D>
-__global__ void __launch_bounds__(64) paged_append_step_kernel(const __grid_constant__ PagedAppendParams p) {
+// One token per sequence: thread = (sequence, head, chunk), the key heads of a
+// sequence first.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int NC = D / 16;
   __shared__ RotaryShared sh;
   load_rotary(&sh, p.rot, D);
-  const long long idx = static_cast<long long>(blockIdx.x) * 64 + threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int hq = p.q ? p.hq : 0, heads = p.hkv + hq;
+  const long long idx = static_cast<long long>(blockIdx.x) * kNrThreads + threadIdx.x;
   const int c = static_cast<int>(idx % NC);
-  const int kvh = static_cast<int>((idx / NC) % p.hkv);
-  const long long bl = idx / NC / p.hkv;
-  const int b = bl < p.batch ? static_cast<int>(bl) : p.batch - 1;
+  const long long last = static_cast<long long>(p.batch) * heads - 1, row = min(idx / NC, last);
+  const int b = static_cast<int>(row / heads), r = static_cast<int>(row % heads);
+  const bool key = r < p.hkv;
   const long long slot = p.start[b];
-  const bool live = bl < p.batch && slot >= 0;
-  const int page = live ? page_of(p, b, slot >> p.page_log2) : -1;
+  const bool live = idx / NC <= last && slot >= 0;
+  const bf16* w = static_cast<const bf16*>(key ? p.k_weight : p.q_weight);
+  Chunk<bf16, kHalf> in, cw;
+  in.load(key ? static_cast<const bf16*>(p.k) + b * p.k_stride + r * D
+              : static_cast<const bf16*>(p.q) + b * p.q_stride + (r - p.hkv) * D, c, D);
+  if (w) cw.load(w, c, D);
+  uint32_t v[8];
+  if (key) load32(v, static_cast<const bf16*>(p.v) + b * p.v_stride + r * D + 16 * c);
+  Position pos;
+  if (p.pos)
+    pos.load(p.pos, p.rot.n_axes, p.tokens, b);
+  else
+    pos.at[0] = static_cast<double>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0.0;
+  const int page = live && key ? page_of(p, b, slot >> p.page_log2) : -1;
   const int at = static_cast<int>(slot & ((1 << p.page_log2) - 1));
-  uint32_t kw[8];
-  append_token<D>(p, &sh, b, slot, kvh, c, page, at, live, kw);
-  if (p.bounds && page >= 0) {
+  uint32_t old[2][8];
+  const bool bound = p.bounds && page >= 0;
+  if (bound && at)  // the page holds earlier keys
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      uint4* row = bounds_row<D>(p, page, kvh, which, c);
-      uint32_t w[8];
+    for (int which = 0; which < 2; ++which)
+      load32(old[which], reinterpret_cast<const bf16*>(bounds_row<D>(p, page, r, which, c)));
+  float cs[8], sn[8], a[8], z[8], wa[8], wb[8];
+  chunk_angles<true>(&sh, c, pos, p.pos ? p.rot.n_axes : 1, cs, sn);
+  in.pairs(a, z);
+  // rows of one warp may have a norm and none: the shuffles are made by all
+  float ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = kw[k];
-      if (at) {  // the page holds earlier keys
-        const uint4 o0 = row[0], o1 = row[1];
-        const uint32_t o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+  for (int k = 0; k < 8; ++k) ss += a[k] * a[k] + z[k] * z[k];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = which ? max_bf16x2(w[k], o[k]) : min_bf16x2(w[k], o[k]);
-      }
-      row[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      row[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+  for (int off = 1; off < NC; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  if (w) {
+    const float scale = rsqrtf(ss * (1.0f / D) + p.eps);
+    cw.pairs(wa, wb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] *= scale * wa[k], z[k] *= scale * wb[k];
+  }
+  norm_rotate<D>(a, z, false, wa, wb, p.eps, cs, sn);
+  uint32_t y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(a[k], z[k]);
+  if (!live) return;
+  if (!key) return store32(static_cast<bf16*>(p.q_out) + (static_cast<long long>(b) * hq + r - p.hkv) * D + 16 * c, y, p.wide);
+  if (page < 0) return;
+  store_slot<D>(p, page, r, c, at, y, v);
+  if (!bound) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = !at ? y[k] : which ? max_bf16x2(y[k], old[1][k]) : min_bf16x2(y[k], old[0][k]);
+    uint4* dst = bounds_row<D>(p, page, r, which, c);
+    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
 
-// Ragged batch: a CTA owns the new tokens of one sequence that fall into one
-// page, for one kv head, so that the page's bounds have one writer.
-template <int D>
+// Ragged batch.  The first p.items * hkv CTAs own each the new tokens of one sequence
+// that fall into one page, for one kv head, so that the page's bounds have one
+// writer; the others kRows query heads each of kNrThreads / (d/16) rows.
+template <int D, bool kHalf>
 __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int NC = D / 16, kTok = kNrThreads / NC;  // tokens in flight
+  constexpr int kWarps = kNrThreads / 32;
   __shared__ RotaryShared sh;
   __shared__ int s_item[3];  // sequence, first row, tokens
-  __shared__ long long s_slot;  // first slot
-  __shared__ uint32_t s_red[2][kNrThreads / 32][D / 2];
-  const int tid = threadIdx.x;
-  // the item's sequence: running count of (sequence, page) items, one warp
-  if (tid < 32) {
-    long long before = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < p.batch && !found; b0 += 32) {
-      const int b = b0 + tid;
-      long long items = 0, r0 = 0, n = 0, s0 = -1;
-      if (b < p.batch) {
-        r0 = p.cu[b];
-        const long long r1 = p.cu[b + 1];
-        s0 = p.start[b];
-        if (r0 < 0 || r1 < r0 || r1 > p.tokens) {
-          atomicCAS(p.err, 0u, kErrBadRows);
-        } else if (s0 >= 0 && r1 > r0) {
-          n = r1 - r0;
-          items = ((s0 + n - 1) >> p.page_log2) - (s0 >> p.page_log2) + 1;
-        }
-      }
-      long long incl = items;
+  __shared__ long long s_slot, s_scan[kWarps];  // first slot
+  __shared__ uint32_t s_red[2][kWarps][D / 2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = tid % NC;
+  const int axes = p.pos ? p.rot.n_axes : 1;
+  load_rotary(&sh, p.rot, D);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const long long kv_blocks = p.items * p.hkv;
+  if (blockIdx.x >= kv_blocks) {
+    // ---- queries
+    const int groups = (p.hq + kRows - 1) / kRows;
+    const long long i = blockIdx.x - kv_blocks;
+    const int h = static_cast<int>(i % groups) * kRows, n = min(kRows, p.hq - h);
+    const long long row0 = i / groups * kTok, row = row0 + tid / NC;
+    const long long t = min(row, static_cast<long long>(p.tokens) - 1);
+    Rows<bf16, D, kRows, kHalf> rows;
+    const bf16* w = static_cast<const bf16*>(p.q_weight);
+    rows.load(static_cast<const bf16*>(p.q) + t * p.q_stride + h * D, n, c, w);
+    // the row's sequence: as many as end at or before it, over all sequences, the
+    // warp's rows side by side
+    constexpr int kPer = 32 / NC;
+    int ended[kPer];
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (tid >= off) incl += o;
-      }
-      const long long mine = static_cast<long long>(blockIdx.x) - before - (incl - items);
-      const bool here = mine >= 0 && mine < items;
-      if (here) {
-        const long long first = mine == 0 ? s0 : ((s0 >> p.page_log2) + mine) << p.page_log2;
-        const long long end = min(s0 + n, ((first >> p.page_log2) + 1) << p.page_log2);
-        s_item[0] = b;
-        s_item[1] = static_cast<int>(r0 + (first - s0));
-        s_item[2] = static_cast<int>(end - first);
-        s_slot = first;
-      }
-      found = __any_sync(0xffffffffu, here);
-      before += __shfl_sync(0xffffffffu, incl, 31);
+    for (int g = 0; g < kPer; ++g) ended[g] = 0;
+    const long long first = row0 + warp * kPer;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int end = b0 + lane < p.batch ? p.cu[b0 + lane + 1] : 0x7fffffff;
+#pragma unroll
+      for (int g = 0; g < kPer; ++g) ended[g] += __popc(__ballot_sync(0xffffffffu, end <= first + g));
     }
-    if (!found && tid == 0) s_item[2] = 0;
+    int b = ended[0];
+#pragma unroll
+    for (int g = 1; g < kPer; ++g) b = lane / NC == g ? ended[g] : b;
+    bool live = row < p.tokens && b < p.batch;
+    long long slot = 0;
+    if (live) {
+      const int r0 = p.cu[b], s0 = p.start[b];
+      live = r0 >= 0 && r0 <= t && s0 >= 0;
+      slot = s0 + (t - r0);
+    }
+    Position pos;
+    if (p.pos)
+      pos.load(p.pos, axes, p.tokens, t);
+    else
+      pos.at[0] = static_cast<double>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0.0;
+    float cs[8], sn[8];
+    chunk_angles<true>(&sh, c, pos, axes, cs, sn);
+    rows.finish(static_cast<bf16*>(p.q_out) + (t * p.hq + h) * D + 16 * c, n, w != nullptr, p.eps, cs, sn, live, p.wide);
+    return;
   }
-  load_rotary(&sh, p.rot, D);  // synchronises
+
+  // ---- keys and values: the item's sequence, by a running count of (sequence, page)
+  const long long item = blockIdx.x / p.hkv;
+  const int kvh = static_cast<int>(blockIdx.x % p.hkv);
+  if (tid == 0) s_item[2] = 0;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.batch && before <= item; b0 += kNrThreads) {
+    const int b = b0 + tid;
+    long long items = 0, r0 = 0, n = 0, s0 = -1;
+    if (b < p.batch) {
+      r0 = p.cu[b];
+      const long long r1 = p.cu[b + 1];
+      s0 = p.start[b];
+      if (r0 < 0 || r1 < r0 || r1 > p.tokens) {
+        atomicCAS(p.err, 0u, kErrBadRows);
+      } else if (s0 >= 0 && r1 > r0) {
+        n = r1 - r0;
+        items = ((s0 + n - 1) >> p.page_log2) - (s0 >> p.page_log2) + 1;
+      }
+    }
+    long long incl = items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    __syncthreads();  // the last round's sums are read
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long mine = item - before - (incl - items);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) mine -= s_scan[w];
+      before += s_scan[w];
+    }
+    if (mine >= 0 && mine < items) {
+      const long long first = mine == 0 ? s0 : ((s0 >> p.page_log2) + mine) << p.page_log2;
+      const long long end = min(s0 + n, ((first >> p.page_log2) + 1) << p.page_log2);
+      s_item[0] = b;
+      s_item[1] = static_cast<int>(r0 + (first - s0));
+      s_item[2] = static_cast<int>(end - first);
+      s_slot = first;
+    }
+  }
+  __syncthreads();
   const int b = s_item[0], row0 = s_item[1], n = s_item[2];
-  const long long slot0 = s_slot;
   if (n == 0) return;
-  const int kvh = blockIdx.y, c = tid % NC;
-  const int page = page_of(p, b, slot0 >> p.page_log2);
+  const long long slot0 = s_slot;
   const int at0 = static_cast<int>(slot0 & ((1 << p.page_log2) - 1));
+  const bf16* w = static_cast<const bf16*>(p.k_weight);
+  // a token ahead: its key, value and positions
+  Chunk<bf16, kHalf> next, cw;
+  uint32_t v_next[8];
+  Position pos_next;
+  auto fetch = [&](int t) {  // clamped: lanes behind the last repeat it
+    const long long tt = min(t, n - 1), row = row0 + tt;
+    next.load(static_cast<const bf16*>(p.k) + row * p.k_stride + kvh * D, c, D);
+    load32(v_next, static_cast<const bf16*>(p.v) + row * p.v_stride + kvh * D + 16 * c);
+    if (p.pos)
+      pos_next.load(p.pos, axes, p.tokens, row);
+    else
+      pos_next.at[0] = static_cast<double>(slot0 + tt), pos_next.at[1] = pos_next.at[2] = pos_next.at[3] = 0.0;
+  };
+  fetch(tid / NC);
+  const int page = page_of(p, b, slot0 >> p.page_log2);
+  if (w) cw.load(w, c, D);
   constexpr uint32_t kInf = 0x7F807F80u, kNegInf = 0xFF80FF80u;
   uint32_t lo[8], hi[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) lo[k] = kInf, hi[k] = kNegInf;
   for (int t0 = 0; t0 < n; t0 += kTok) {
     const int t = t0 + tid / NC;
-    const bool live = t < n;
-    const int tt = live ? t : n - 1;
-    uint32_t kw[8];
-    append_token<D>(p, &sh, row0 + tt, slot0 + tt, kvh, c, page, at0 + tt, live, kw);
+    const Chunk<bf16, kHalf> in = next;
+    const Position pos = pos_next;
+    uint32_t v[8], y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {  // a clamped lane repeats the last token's key
-      lo[k] = min_bf16x2(lo[k], kw[k]);
-      hi[k] = max_bf16x2(hi[k], kw[k]);
+    for (int k = 0; k < 8; ++k) v[k] = v_next[k];
+    if (t0 + kTok < n) fetch(t + kTok);
+    float cs[8], sn[8], a[8], z[8], wa[8], wb[8];
+    chunk_angles<true>(&sh, c, pos, axes, cs, sn);
+    if (w) cw.pairs(wa, wb);
+    in.pairs(a, z);
+    norm_rotate<D>(a, z, w != nullptr, wa, wb, p.eps, cs, sn);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = pack_bf16x2(a[k], z[k]);
+      lo[k] = min_bf16x2(lo[k], y[k]);
+      hi[k] = max_bf16x2(hi[k], y[k]);
     }
+    if (t < n && page >= 0) store_slot<D>(p, page, kvh, c, at0 + t, y, v);
   }
   if (!p.bounds || page < 0) return;
 #pragma unroll
@@ -397,38 +531,41 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_c
       lo[k] = min_bf16x2(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], off));
       hi[k] = max_bf16x2(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], off));
     }
-  if ((tid & 31) < NC) {
+  if (lane < NC) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      s_red[0][tid >> 5][8 * c + k] = lo[k];
-      s_red[1][tid >> 5][8 * c + k] = hi[k];
+      s_red[0][warp][8 * c + k] = lo[k];
+      s_red[1][warp][8 * c + k] = hi[k];
     }
   }
   __syncthreads();
   for (int i = tid; i < D; i += kNrThreads) {  // word i % (D/2) of the minima, then of the maxima
-    const int which = i / (D / 2), w = i % (D / 2);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(bounds_row<D>(p, page, kvh, which, 0)) + w;
-    uint32_t r = s_red[which][0][w];
-    for (int k = 1; k < kNrThreads / 32; ++k) r = which ? max_bf16x2(r, s_red[1][k][w]) : min_bf16x2(r, s_red[0][k][w]);
+    const int which = i / (D / 2), x = i % (D / 2);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(bounds_row<D>(p, page, kvh, which, 0)) + x;
+    uint32_t r = s_red[which][0][x];
+    for (int k = 1; k < kWarps; ++k) r = which ? max_bf16x2(r, s_red[1][k][x]) : min_bf16x2(r, s_red[0][k][x]);
     if (at0) r = which ? max_bf16x2(r, *dst) : min_bf16x2(r, *dst);
     *dst = r;
   }
 }
 
+long long paged_append_blocks(const PagedAppendParams& p) {
+  const int tok = kNrThreads / (p.d / 16), groups = p.q ? (p.hq + kRows - 1) / kRows : 0;
+  return p.items * p.hkv + (p.tokens + tok - 1LL) / tok * groups;
+}
+
+template <int D, bool kHalf>
+static cudaError_t launch_append(const PagedAppendParams& p, cudaStream_t s) {
+  if (p.cu)
+    return launch_pdl(paged_append_kernel<D, kHalf>, static_cast<unsigned>(paged_append_blocks(p)), kNrThreads, 0, s, p);
+  const long long threads = static_cast<long long>(p.batch) * (p.hkv + (p.q ? p.hq : 0)) * (D / 16);
+  return launch_pdl(paged_append_step_kernel<D, kHalf>, static_cast<unsigned>((threads + kNrThreads - 1) / kNrThreads), kNrThreads,
+                    0, s, p);
+}
+
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
-  if (!p.cu) {
-    const long long threads = static_cast<long long>(p.batch) * p.hkv * (p.d / 16);
-    const unsigned blocks = static_cast<unsigned>((threads + 63) / 64);
-    p.d == 64 ? paged_append_step_kernel<64><<<blocks, 64, 0, s>>>(p)
-              : paged_append_step_kernel<128><<<blocks, 64, 0, s>>>(p);
-  } else {
-    // a sequence with n > 0 new tokens touches at most (n - 1) / page + 2 pages
-    const long long items = (p.tokens >> p.page_log2) + 2LL * (p.batch < p.tokens ? p.batch : p.tokens);
-    const dim3 grid(static_cast<unsigned>(items), p.hkv);
-    p.d == 64 ? paged_append_kernel<64><<<grid, kNrThreads, 0, s>>>(p)
-              : paged_append_kernel<128><<<grid, kNrThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  if (p.d == 64) return p.pairing ? launch_append<64, true>(p, s) : launch_append<64, false>(p, s);
+  return p.pairing ? launch_append<128, true>(p, s) : launch_append<128, false>(p, s);
 }
 
 }  // namespace atf

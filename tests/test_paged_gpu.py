@@ -97,6 +97,33 @@ def test_norm_rope_without_norm_agrees_with_the_rope_kernel():
             assert torch.allclose(y.float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -13)
 
 
+def _offset(x, n):
+    """A copy of x that starts n elements into its storage."""
+    buf = torch.empty(x.numel() + n, dtype=x.dtype, device=x.device)
+    return buf[n:].view(x.shape).copy_(x)
+
+
+def test_rows_aligned_to_16_bytes_only():
+    """Outputs and pages that no 32-byte store may touch."""
+    T, Hq, Hkv, d, page = 40, 6, 2, 128, 16
+    pos = torch.arange(T, device="cuda")[None]
+    for dtype, n in ((BF16, 8), (torch.float32, 4)):
+        q, k = _normal(11, T, Hq, d, dtype=dtype), _normal(12, T, Hkv, d, dtype=dtype)
+        want = atf.qk_norm_rope(q, k, 1e4, pos)
+        got = atf.qk_norm_rope(_offset(q, n), _offset(k, n), 1e4, pos, q_out=_offset(q, n), k_out=_offset(k, n))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    q, k, v = (_normal(s, T, h, d) for s, h in ((13, Hq), (14, Hkv), (15, Hkv)))
+    table = _int32([[2, 0, 1]])
+    for cu, at in ((_int32([0, T]), slice(0, T)), (None, slice(0, 1))):
+        out = []
+        for n in (0, 8):
+            kp, vp = (_offset(x, n) for x in _pool(3, Hkv, d, page, 16))
+            qo = atf.paged_append(q[at], k[at], v[at], kp, vp, table, _int32([3]), 1e4, cu=cu, q_out=_offset(q[at], n))
+            out.append((qo, kp, vp))
+        atf.atf_check()
+        assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
 def test_norm_rope_feeds_the_prefill():
     S, Hq, Hkv, d, theta, alpha = 300, 14, 2, 128, 1e4, 1.0
     q, k, v = _normal(7, S, Hq, d), _normal(8, S, Hkv, d), _normal(9, S, Hkv, d)
