@@ -73,10 +73,10 @@ struct AppendParams {
 };
 
 // Rotation angles of up to four position axes: pair i of a token turns by
-// pos[axis of i] * theta^(-2i/d), held in turns.
+// pos[axis of i] * theta^(-2i/d), held in turns of 2^64.
 constexpr int kMaxAxes = 4;
 struct RotaryTable {
-  double turns[kMaxPairs];          // theta^(-2i/d) / (2 pi)
+  unsigned long long turns[kMaxPairs];  // round(2^64 theta^(-2i/d) / (2 pi))
   unsigned char axis[kMaxPairs];    // < kMaxAxes
   int n_axes;
 };

@@ -50,14 +50,18 @@ atf_status rotary_table(const char* who, int d, double theta, int n_axes, const 
     return report_error(ATF_ERR_UNSUPPORTED, "%s: n_axes %d outside [1, %d]", who, n_axes, kMaxAxes);
   if (n_axes > 1 && !pair_axis)
     return report_error(ATF_ERR_INVALID_ARG, "%s: several position axes need pair_axis", who);
-  const double two_pi = 6.283185307179586476925286766559;
+  const long double turn = 18446744073709551616.0L / 6.283185307179586476925286766559L;  // 2^64 / (2 pi)
   // a thread's calls mostly share d and theta; the powers take longer than the launch
   static thread_local struct {
     int d = 0;
-    double theta = 0.0, turns[kMaxPairs] = {};
+    double theta = 0.0;
+    unsigned long long turns[kMaxPairs] = {};
   } last;
   if (last.d != d || last.theta != theta) {
-    for (int i = 0; i < kMaxPairs; ++i) last.turns[i] = i < d / 2 ? std::pow(theta, -2.0 * i / d) / two_pi : 0.0;
+    for (int i = 0; i < kMaxPairs; ++i)
+      last.turns[i] = i < d / 2 ? static_cast<unsigned long long>(
+                                      std::round(std::pow(static_cast<long double>(theta), -2.0L * i / d) * turn))
+                                : 0ull;
     last.d = d;
     last.theta = theta;
   }

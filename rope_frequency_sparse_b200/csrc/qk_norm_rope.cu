@@ -5,8 +5,10 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w           (per head; skipped without w)
 //   (y_a, y_b) of pair i turned by pos[axis(i)] * theta^(-2i/d)
 //
-// all in fp32 and rounded once.  The angle is reduced to a fraction of a turn in
-// fp64 (at position 2^20 an fp32 angle is off by more than a bf16 step).  The sine
+// all in fp32 and rounded once.  The angle is reduced to a fraction of a turn by a
+// 64-bit integer product that wraps (at position 2^20 an fp32 angle is off by more
+// than a bf16 step; the product is off by 2^-34 turns at 2^31, and takes a third of
+// the time of fp64's multiply, round and convert).  The sine
 // and cosine of that fraction are fp32's for fp32 rows; for bf16 rows the fast ones,
 // off by at most 2^-21 on [-pi, pi], 2^-13 of a bf16 half step.
 //
@@ -15,8 +17,8 @@
 // d/2+8c..d/2+8c+7 (rotate-half), which are the 16 outputs 16c..16c+15 either way and
 // one 32-byte row of the key pages, written by one store.  It evaluates the chunk's
 // eight angles once for up to kRows heads, whose loads are all under way before the
-// first is used (one at a time: 32 us for 8192 tokens of 28 + 4 heads of 128, 20.5 at
-// the copy rate); the d/16 lanes of a head add their squares by shuffles.  Few rows
+// first is used (8192 tokens of 28 + 4 heads of 128: 23.9 us, 32 with one load at a
+// time, 20.5 at the copy rate); the d/16 lanes of a head add their squares by shuffles.  Few rows
 // take one head a thread: there the latency of a thread's chain is what counts.
 #include <cuda_bf16.h>
 
@@ -102,73 +104,108 @@ struct Chunk<float, kHalf> {
 };
 
 struct RotaryShared {
-  double turns[kMaxPairs];
-  unsigned char axis[kMaxPairs];
+  unsigned long long turns[kMaxPairs];  // pair 8 c + k at k * (d/16) + c: a warp's chunks side by side
+  signed char axis[kMaxPairs];
+  signed char chunk_axis[kMaxPairs / 8];  // of all the chunk's pairs, or -1: several
 };
 
-__device__ __forceinline__ void load_rotary(RotaryShared* sh, const RotaryTable& rot, int d) {
-  for (int i = threadIdx.x; i < d / 2; i += blockDim.x) {
-    sh->turns[i] = rot.turns[i];
-    sh->axis[i] = rot.axis[i];
+template <int D>
+__device__ __forceinline__ void load_rotary(RotaryShared* sh, const RotaryTable& rot) {
+  constexpr int NC = D / 16;
+  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) {
+    sh->turns[(i & 7) * NC + (i >> 3)] = rot.turns[i];
+    sh->axis[(i & 7) * NC + (i >> 3)] = static_cast<signed char>(rot.axis[i]);
+  }
+  if (threadIdx.x < NC) {
+    int a = rot.axis[8 * threadIdx.x];
+    for (int k = 1; k < 8; ++k) a = rot.axis[8 * threadIdx.x + k] == a ? a : -1;
+    sh->chunk_axis[threadIdx.x] = static_cast<signed char>(a);
   }
   __syncthreads();
 }
 
 // Positions of a token on up to kMaxAxes axes.
 struct Position {
-  double at[kMaxAxes];
+  int at[kMaxAxes];
   __device__ __forceinline__ void load(const long long* pos, int n_axes, long long tokens, long long t) {
 #pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) at[a] = a < n_axes ? static_cast<double>(pos[a * tokens + t]) : 0.0;
+    for (int a = 0; a < kMaxAxes; ++a) at[a] = a < n_axes ? static_cast<int>(pos[a * tokens + t]) : 0;
   }
 };
 
-// Cosine and sine of the eight angles of chunk c.
-template <bool kFast>
-__device__ __forceinline__ void chunk_angles(const RotaryShared* sh, int c, const Position& pos, int n_axes, float* cs, float* sn) {
+// Norm weights and rotation of a chunk's eight pairs as one map, two pairs a word:
+// a' = a ac + b bs, b' = a as + b bc.
+struct Turn {
+  uint64_t ac[4], bs[4], as[4], bc[4];
+};
+
+template <int D, bool kFast>
+__device__ __forceinline__ void chunk_turn(Turn& turn, const RotaryShared* sh, int c, const Position& pos, int n_axes, bool norm,
+                                           const float* wa, const float* wb) {
+  constexpr int NC = D / 16;
+  const int chunk = n_axes > 1 ? sh->chunk_axis[c] : 0;
+  auto on_axis = [&](int a) { return a == 1 ? pos.at[1] : a == 2 ? pos.at[2] : a == 3 ? pos.at[3] : pos.at[0]; };
+  const int common = on_axis(chunk);
+  float m[4][8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    double p = pos.at[0];
-    if (n_axes > 1) {
-      const int a = sh->axis[8 * c + k];
-      p = a == 1 ? pos.at[1] : a == 2 ? pos.at[2] : a == 3 ? pos.at[3] : p;
-    }
-    const double t = p * sh->turns[8 * c + k];
-    const float turn = static_cast<float>(t - rint(t));
+    int p = common;
+    if (chunk < 0) p = on_axis(sh->axis[k * NC + c]);
+    const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(p)) * sh->turns[k * NC + c];
+    const float part = static_cast<float>(static_cast<int>(t >> 32));  // of 2^32 of a turn, in [-1/2, 1/2)
+    float sn, cs;
     if (kFast) {
-      const float x = 6.283185307f * turn;
-      sn[k] = __sinf(x);
-      cs[k] = __cosf(x);
+      const float x = 1.4629180792671596e-9f * part;  // 2 pi / 2^32
+      sn = __sinf(x);
+      cs = __cosf(x);
     } else {
-      sincospif(2.0f * turn, &sn[k], &cs[k]);
+      sincospif(4.656612873077393e-10f * part, &sn, &cs);  // 2 / 2^32
     }
+    m[0][k] = norm ? wa[k] * cs : cs;
+    m[1][k] = norm ? -wb[k] * sn : -sn;
+    m[2][k] = norm ? wa[k] * sn : sn;
+    m[3][k] = norm ? wb[k] * cs : cs;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    turn.ac[k] = pack2(m[0][2 * k], m[0][2 * k + 1]);
+    turn.bs[k] = pack2(m[1][2 * k], m[1][2 * k + 1]);
+    turn.as[k] = pack2(m[2][2 * k], m[2][2 * k + 1]);
+    turn.bc[k] = pack2(m[3][2 * k], m[3][2 * k + 1]);
   }
 }
 
-// Norm (with weights wa, wb of the eight pairs) and rotation of one head's chunk
-// over the d/16 neighbouring lanes of the head; every lane of the warp calls it.
+// One over the root mean square of a head whose chunks the d/16 neighbouring lanes
+// hold; every lane of the warp calls it.
 template <int D>
-__device__ __forceinline__ void norm_rotate(float* a, float* b, bool norm, const float* wa, const float* wb, float eps,
-                                            const float* cs, const float* sn) {
-  if (norm) {
-    float ss = 0.f;
+__device__ __forceinline__ float norm_scale(const uint64_t* a, const uint64_t* b, float eps) {
+  uint64_t s2 = fmul2(a[0], a[0]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss += a[k] * a[k] + b[k] * b[k];
-#pragma unroll
-    for (int off = 1; off < D / 16; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float r = rsqrtf(ss * (1.0f / D) + eps);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      a[k] *= r * wa[k];
-      b[k] *= r * wb[k];
-    }
+  for (int k = 0; k < 4; ++k) {
+    if (k) s2 = ffma2(a[k], a[k], s2);
+    s2 = ffma2(b[k], b[k], s2);
   }
+  float x, y;
+  unpack2(s2, x, y);
+  x += y;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float x = a[k], y = b[k];
-    a[k] = x * cs[k] - y * sn[k];
-    b[k] = x * sn[k] + y * cs[k];
+  for (int off = 1; off < D / 16; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return rsqrtf(x * (1.0f / D) + eps);
+}
+
+// The chunk of one head, turned and scaled: the first components to ya, the second to yb.
+__device__ __forceinline__ void apply(const Turn& t, const uint64_t* a, const uint64_t* b, float scale, float* ya, float* yb) {
+  const uint64_t r = pack2(scale, scale);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    unpack2(fmul2(r, ffma2(a[k], t.ac[k], fmul2(b[k], t.bs[k]))), ya[2 * k], ya[2 * k + 1]);
+    unpack2(fmul2(r, ffma2(a[k], t.as[k], fmul2(b[k], t.bc[k]))), yb[2 * k], yb[2 * k + 1]);
   }
+}
+
+__device__ __forceinline__ void pack_pairs(const float* x, uint64_t* y) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = pack2(x[2 * k], x[2 * k + 1]);
 }
 
 // A token's chunk of up to R neighbouring heads and their weights.
@@ -180,17 +217,23 @@ struct Rows {
     for (int r = 0; r < R; ++r) in[r].load(x + (R == 1 ? 0 : min(r, n - 1)) * D, c, D);
     if (w) weight.load(w, c, D);
   }
-  // Heads r < n to out + r * d, where `live`; every lane of the warp calls it.
-  __device__ __forceinline__ void finish(T* out, int n, bool norm, float eps, const float* cs, const float* sn, bool live,
-                                         bool wide) const {
+  template <bool kFast>
+  __device__ __forceinline__ void turn(Turn& t, const RotaryShared* sh, int c, const Position& pos, int n_axes, bool norm) const {
     float wa[8], wb[8];
     if (norm) weight.pairs(wa, wb);
+    chunk_turn<D, kFast>(t, sh, c, pos, n_axes, norm, wa, wb);
+  }
+  // Heads r < n to out + r * d, where `live`; every lane of the warp calls it.
+  __device__ __forceinline__ void finish(T* out, int n, const Turn& t, bool norm, float eps, bool live, bool wide) const {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float a[8], b[8];
-      in[r].pairs(a, b);
-      norm_rotate<D>(a, b, norm, wa, wb, eps, cs, sn);
-      if (live && r < n) Chunk<T, kHalf>::store(out + r * D, a, b, wide);
+      float x[8], y[8];
+      uint64_t a[4], b[4];
+      in[r].pairs(x, y);
+      pack_pairs(x, a);
+      pack_pairs(y, b);
+      apply(t, a, b, norm ? norm_scale<D>(a, b, eps) : 1.f, x, y);
+      if (live && r < n) Chunk<T, kHalf>::store(out + r * D, x, y, wide);
     }
   }
 };
@@ -198,12 +241,13 @@ struct Rows {
 }  // namespace
 
 // Dense form.  Thread = (token, chunk), blockIdx.y = R query heads or, behind them, R
-// key heads.
+// key heads.  Registers for six CTAs an SM (four in fp32), five in the append below: its
+// 32768 tokens of five prompts take 144 us at the three that fit unbounded, 110 at five.
 template <typename T, int D, int R, bool kHalf>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 6 : 4) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int NC = D / 16;
   __shared__ RotaryShared sh;
-  load_rotary(&sh, p.rot, D);
+  load_rotary<D>(&sh, p.rot);
   pdl_launch_dependents();
   pdl_wait();
   const long long idx = static_cast<long long>(blockIdx.x) * kNrThreads + threadIdx.x;
@@ -218,10 +262,9 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const __grid_c
   rows.load(static_cast<const T*>(key ? p.k : p.q) + t * (key ? p.k_stride : p.q_stride) + h * D, n, c, w);
   Position pos;
   pos.load(p.pos, p.rot.n_axes, p.tokens, t);
-  float cs[8], sn[8];
-  chunk_angles<sizeof(T) == 2>(&sh, c, pos, p.rot.n_axes, cs, sn);
-  rows.finish(static_cast<T*>(key ? p.k_out : p.q_out) + (t * heads + h) * D + 16 * c, n, w != nullptr, p.eps, cs, sn, live,
-              p.wide);
+  Turn turn;
+  rows.template turn<sizeof(T) == 2>(turn, &sh, c, pos, p.rot.n_axes, w != nullptr);
+  rows.finish(static_cast<T*>(key ? p.k_out : p.q_out) + (t * heads + h) * D + 16 * c, n, turn, w != nullptr, p.eps, live, p.wide);
 }
 
 template <typename T, int D, bool kHalf>
@@ -306,7 +349,7 @@ template <int D, bool kHalf>
 __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int NC = D / 16;
   __shared__ RotaryShared sh;
-  load_rotary(&sh, p.rot, D);
+  load_rotary<D>(&sh, p.rot);
   pdl_launch_dependents();
   pdl_wait();
   const int hq = p.q ? p.hq : 0, heads = p.hkv + hq;
@@ -328,7 +371,7 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
   if (p.pos)
     pos.load(p.pos, p.rot.n_axes, p.tokens, b);
   else
-    pos.at[0] = static_cast<double>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0.0;
+    pos.at[0] = static_cast<int>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0;
   const int page = live && key ? page_of(p, b, slot >> p.page_log2) : -1;
   const int at = static_cast<int>(slot & ((1 << p.page_log2) - 1));
   uint32_t old[2][8];
@@ -337,25 +380,19 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
 #pragma unroll
     for (int which = 0; which < 2; ++which)
       load32(old[which], reinterpret_cast<const bf16*>(bounds_row<D>(p, page, r, which, c)));
-  float cs[8], sn[8], a[8], z[8], wa[8], wb[8];
-  chunk_angles<true>(&sh, c, pos, p.pos ? p.rot.n_axes : 1, cs, sn);
-  in.pairs(a, z);
-  // rows of one warp may have a norm and none: the shuffles are made by all
-  float ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) ss += a[k] * a[k] + z[k] * z[k];
-#pragma unroll
-  for (int off = 1; off < NC; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  if (w) {
-    const float scale = rsqrtf(ss * (1.0f / D) + p.eps);
-    cw.pairs(wa, wb);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] *= scale * wa[k], z[k] *= scale * wb[k];
-  }
-  norm_rotate<D>(a, z, false, wa, wb, p.eps, cs, sn);
+  float x[8], z[8], wa[8], wb[8];
+  uint64_t x2[4], z2[4];
+  Turn turn;
+  if (w) cw.pairs(wa, wb);
+  chunk_turn<D, true>(turn, &sh, c, pos, p.pos ? p.rot.n_axes : 1, w != nullptr, wa, wb);
+  in.pairs(x, z);
+  pack_pairs(x, x2);
+  pack_pairs(z, z2);
+  const float scale = norm_scale<D>(x2, z2, p.eps);  // a warp's rows may have a norm and none
+  apply(turn, x2, z2, w ? scale : 1.f, x, z);
   uint32_t y[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(a[k], z[k]);
+  for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[k], z[k]);
   if (!live) return;
   if (!key) return store32(static_cast<bf16*>(p.q_out) + (static_cast<long long>(b) * hq + r - p.hkv) * D + 16 * c, y, p.wide);
   if (page < 0) return;
@@ -363,12 +400,12 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
   if (!bound) return;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    uint32_t x[8];
+    uint32_t m[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = !at ? y[k] : which ? max_bf16x2(y[k], old[1][k]) : min_bf16x2(y[k], old[0][k]);
+    for (int k = 0; k < 8; ++k) m[k] = !at ? y[k] : which ? max_bf16x2(y[k], old[1][k]) : min_bf16x2(y[k], old[0][k]);
     uint4* dst = bounds_row<D>(p, page, r, which, c);
-    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    dst[0] = make_uint4(m[0], m[1], m[2], m[3]);
+    dst[1] = make_uint4(m[4], m[5], m[6], m[7]);
   }
 }
 
@@ -376,7 +413,7 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
 // that fall into one page, for one kv head, so that the page's bounds have one
 // writer; the others kRows query heads each of kNrThreads / (d/16) rows.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+__global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int NC = D / 16, kTok = kNrThreads / NC;  // tokens in flight
   constexpr int kWarps = kNrThreads / 32;
   __shared__ RotaryShared sh;
@@ -385,7 +422,7 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_c
   __shared__ uint32_t s_red[2][kWarps][D / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = tid % NC;
   const int axes = p.pos ? p.rot.n_axes : 1;
-  load_rotary(&sh, p.rot, D);
+  load_rotary<D>(&sh, p.rot);
   pdl_launch_dependents();
   pdl_wait();
 
@@ -426,10 +463,10 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_c
     if (p.pos)
       pos.load(p.pos, axes, p.tokens, t);
     else
-      pos.at[0] = static_cast<double>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0.0;
-    float cs[8], sn[8];
-    chunk_angles<true>(&sh, c, pos, axes, cs, sn);
-    rows.finish(static_cast<bf16*>(p.q_out) + (t * p.hq + h) * D + 16 * c, n, w != nullptr, p.eps, cs, sn, live, p.wide);
+      pos.at[0] = static_cast<int>(slot), pos.at[1] = pos.at[2] = pos.at[3] = 0;
+    Turn turn;
+    rows.template turn<true>(turn, &sh, c, pos, axes, w != nullptr);
+    rows.finish(static_cast<bf16*>(p.q_out) + (t * p.hq + h) * D + 16 * c, n, turn, w != nullptr, p.eps, live, p.wide);
     return;
   }
 
@@ -493,7 +530,7 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_c
     if (p.pos)
       pos_next.load(p.pos, axes, p.tokens, row);
     else
-      pos_next.at[0] = static_cast<double>(slot0 + tt), pos_next.at[1] = pos_next.at[2] = pos_next.at[3] = 0.0;
+      pos_next.at[0] = static_cast<int>(slot0 + tt), pos_next.at[1] = pos_next.at[2] = pos_next.at[3] = 0;
   };
   fetch(tid / NC);
   const int page = page_of(p, b, slot0 >> p.page_log2);
@@ -510,14 +547,18 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = v_next[k];
     if (t0 + kTok < n) fetch(t + kTok);
-    float cs[8], sn[8], a[8], z[8], wa[8], wb[8];
-    chunk_angles<true>(&sh, c, pos, axes, cs, sn);
+    float x[8], z[8], wa[8], wb[8];
+    uint64_t x2[4], z2[4];
+    Turn turn;
     if (w) cw.pairs(wa, wb);
-    in.pairs(a, z);
-    norm_rotate<D>(a, z, w != nullptr, wa, wb, p.eps, cs, sn);
+    chunk_turn<D, true>(turn, &sh, c, pos, axes, w != nullptr, wa, wb);
+    in.pairs(x, z);
+    pack_pairs(x, x2);
+    pack_pairs(z, z2);
+    apply(turn, x2, z2, w ? norm_scale<D>(x2, z2, p.eps) : 1.f, x, z);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      y[k] = pack_bf16x2(a[k], z[k]);
+      y[k] = pack_bf16x2(x[k], z[k]);
       lo[k] = min_bf16x2(lo[k], y[k]);
       hi[k] = max_bf16x2(hi[k], y[k]);
     }
