@@ -115,7 +115,8 @@ struct PagedDecodeParams {
   const int *page_table, *kv_len, *selected;  // selected nullable: [batch][hkv][n_sel] logical pages
   void* out;              // [batch][hq][d] bf16
   float* lse;             // nullable [batch][hq]
-  float* partials;        // [kPagedCtas][2][8][d + 2]
+  float* partials;        // [kPagedCtas][2][8][d] weighted sums of the pieces
+  float2* sums;           // [kPagedCtas][2][8] their maxima and row sums
   int4* meta;             // [kPagedCtas]: split sequence, kv head, last CTA of the sequences begun by each CTA
   int batch, hq, hkv, d, page_log2, max_pages, num_pages, n_sel;
   unsigned int* err;

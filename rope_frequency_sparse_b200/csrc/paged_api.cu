@@ -270,6 +270,7 @@ atf_status atf_paged_decode(const atf_paged_decode_args* a, void* stream) {
   p.lse = a->lse;
   p.meta = static_cast<int4*>(a->workspace);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + kMetaBytes);
+  p.sums = reinterpret_cast<float2*>(p.partials + kPagedCtas * 2 * 8 * a->d);
   p.batch = a->batch;
   p.hq = a->heads;
   p.hkv = a->kv_heads;

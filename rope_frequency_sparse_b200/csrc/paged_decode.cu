@@ -41,12 +41,14 @@ namespace atf {
 
 namespace {
 
-constexpr int kPdConsumers = 8;  // two groups of four warps, 16 keys of a tile apiece
+constexpr int kPdGroups = 2;  // of four warps, 16 keys of a tile apiece
+constexpr int kPdConsumers = 4 * kPdGroups;
 constexpr int kPdProducers = 4;  // warps that fill the ring, every fourth tile each
 constexpr int kPdThreads = (kPdConsumers + kPdProducers) * 32;
 constexpr int kTileKeys = kPagedTileKeys;
 constexpr int kTileLog2 = 6;
 static_assert(1 << kTileLog2 == kTileKeys, "tile");
+constexpr int kPerLane = 4;  // sequences that a lane sums in a small batch
 constexpr int kMaxTilePages = 4;  // boxes of 16 keys
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -82,7 +84,8 @@ struct PdShared {
   long long scan[kPdThreads / 32];
   int start_b, start_len;  // the sequence that this CTA's piece begins in (-1: no piece)
   long long start_base;
-  float mw[kPdConsumers][8], lw[kPdConsumers][8];
+  float mw[kPdConsumers][8], lw[kPdConsumers][8];  // maxima and row sums of the warps
+  float m[8], l[8];                                // and of all, joined
 };
 
 template <int D>
@@ -129,22 +132,16 @@ __device__ __forceinline__ int tile_weight(const PagedDecodeParams& p, const int
   return x;
 }
 
-// Smallest t in [0, tiles] with tile_weight(t) >= x.
+// Smallest t in [0, tiles] with tile_weight(t) >= x, by a warp: 32 points at a time.
 template <int NC>
 __device__ __forceinline__ int tile_at(const PagedDecodeParams& p, const int* w, int len, int tiles, int x) {
-  int dead[NC];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, (len - w[8 * c + 7] - 1) / kTileKeys);
   int lo = 0, hi = tiles;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    int y = 2 * NC * mid;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) y -= min(mid, dead[c]);
-    if (y >= x)
-      hi = mid;
-    else
-      lo = mid + 1;
+    const int step = (hi - lo + 32) >> 5;  // hi is a candidate too
+    const int t = min(hi, lo + static_cast<int>(threadIdx.x & 31) * step + step - 1);
+    const int first = __ffs(__ballot_sync(0xffffffffu, t >= hi || tile_weight<NC>(p, w, len, t) >= x)) - 1;
+    lo += first * step;
+    hi = min(hi, lo + step - 1);
   }
   return lo;
 }
@@ -231,49 +228,82 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   }
   if (tid == kPdConsumers * 32) prefetch_tmap(&tm_k), prefetch_tmap(&tm_v);
   for (int i = tid; i < kMaxPairs; i += kPdThreads) sh->w[i] = p.win.w[i];
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- where this CTA's piece of the tile list begins
-  const int per = (p.batch + kPdThreads - 1) / kPdThreads;  // sequences a thread sums
-  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-  const int len0 = b0 < b1 ? clamped_len(p, b0) : 0;
-  __syncthreads();
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int len = b == b0 ? len0 : clamped_len(p, b);
-    mine += static_cast<long long>(tile_weight<NC>(p, sh->w, len, tiles_of(p, len))) * p.hkv;
-  }
-  long long incl = mine;
+  // ---- where this CTA's piece of the tile list begins: the sequences' weights, summed
+  // up to each.  Small batches are summed by every producer warp for itself, which
+  // needs no barrier (two barriers and the block's sums took 0.9 us of a call's 9)
+  const bool alone = p.batch <= 32 * kPerLane;
+  long long total = 0, base = 0;  // weight of all, and before the piece's first sequence
+  int b = -1, len = 0;            // the piece's first sequence (-1: no piece)
+  auto weight_of = [&](int n) { return static_cast<long long>(tile_weight<NC>(p, sh->w, n, tiles_of(p, n))) * p.hkv; };
+  auto scan = [&](long long x) {  // inclusive, over the warp
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) sh->scan[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - mine;
-#pragma unroll
-  for (int i = 0; i < kPdThreads / 32; ++i) {
-    if (i < warp) before += sh->scan[i];
-    total += sh->scan[i];
-  }
-  const long long from = piece_begin(total, cta), to = piece_begin(total, cta + 1);
-  if (from < to && from >= before && from < before + mine) {
-    long long base = before;
-    for (int b = b0; b < b1; ++b) {
-      const int len = b == b0 ? len0 : clamped_len(p, b);
-      const long long x = static_cast<long long>(tile_weight<NC>(p, sh->w, len, tiles_of(p, len))) * p.hkv;
-      if (from < base + x) {
-        sh->start_b = b;
-        sh->start_len = len;
-        sh->start_base = base;
-        break;
-      }
-      base += x;
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += o;
     }
+    return x;
+  };
+  if (alone) {
+    if (warp >= kPdConsumers) {
+      int n[kPerLane];
+      long long x[kPerLane], mine = 0;
+      const int per = (p.batch + 31) >> 5;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) n[j] = j < per && lane * per + j < p.batch ? clamped_len(p, lane * per + j) : -1;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) mine += x[j] = n[j] >= 0 ? weight_of(n[j]) : 0;
+      const long long incl = scan(mine);
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      const long long from = piece_begin(total, cta);
+      long long at = incl - mine;
+      const unsigned holds = __ballot_sync(0xffffffffu, from < piece_begin(total, cta + 1) && from >= at && from < incl);
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) {
+        if (b < 0 && n[j] >= 0 && from < at + x[j]) b = lane * per + j, len = n[j], base = at;
+        at += x[j];
+      }
+      const int src = holds ? __ffs(holds) - 1 : 0;
+      b = __shfl_sync(0xffffffffu, holds ? b : -1, src);
+      len = __shfl_sync(0xffffffffu, len, src);
+      base = __shfl_sync(0xffffffffu, base, src);
+    }
+  } else {
+    const int per = (p.batch + kPdThreads - 1) / kPdThreads;  // sequences a thread sums
+    const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+    long long mine = 0;
+    for (int i = b0; i < b1; ++i) mine += weight_of(clamped_len(p, i));
+    const long long incl = scan(mine);
+    if (lane == 31) sh->scan[warp] = incl;
+    __syncthreads();
+    long long at = incl - mine;
+#pragma unroll
+    for (int i = 0; i < kPdThreads / 32; ++i) {
+      if (i < warp) at += sh->scan[i];
+      total += sh->scan[i];
+    }
+    const long long from = piece_begin(total, cta);
+    if (from < piece_begin(total, cta + 1) && from >= at && from < at + mine) {
+      for (int i = b0; i < b1; ++i) {
+        const int n = clamped_len(p, i);
+        const long long x = weight_of(n);
+        if (from < at + x) {
+          sh->start_b = i;
+          sh->start_len = n;
+          sh->start_base = at;
+          break;
+        }
+        at += x;
+      }
+    }
+    __syncthreads();
+    b = sh->start_b;
+    len = sh->start_len;
+    base = sh->start_base;
   }
-  __syncthreads();
 
   if (warp >= kPdConsumers) {
     // ================================================================ producer
@@ -283,9 +313,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     bool ok = true, has_partial0 = false, has_meta = false;
     const int ps = 1 << p.page_log2, sub_log2 = p.page_log2 - box_log2, boxes = kTileKeys >> box_log2;
     const uint32_t box_bytes = static_cast<uint32_t>(D * 2) << box_log2;
-    int b = sh->start_b, hk = 0, len = sh->start_len;
+    const long long from = piece_begin(total, cta), to = piece_begin(total, cta + 1);
+    int hk = 0;
     bool more = b >= 0;
-    long long base = more ? sh->start_base : 0;  // weight before (b, hk)
     while (more && ok) {
       const int tiles = tiles_of(p, len);
       const int unit = tile_weight<NC>(p, sh->w, len, tiles);
@@ -293,25 +323,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       const int t0 = from > base ? tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(from - base)) : 0;
       const int t1 = to >= base + unit ? tiles : tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
-        int slot = -1;
-        if (t0 > 0) {
-          slot = 0;
-          has_partial0 = true;
-        } else if (t1 < tiles) {
-          slot = 1;
-          has_meta = true;
-          const long long x = base + tile_weight<NC>(p, sh->w, len, tiles - 1);  // where its last tile begins
-          // the CTA whose piece holds x: the largest j with piece_begin(j) <= x
-          int lo = cta, hi = kPagedCtas - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (piece_begin(total, mid) <= x)
-              lo = mid;
-            else
-              hi = mid - 1;
-          }
-          if (pw == 0 && lane == 0) p.meta[cta] = make_int4(b, hk, lo, 0);
-        }
+        const int slot = t0 > 0 ? 0 : t1 < tiles ? 1 : -1;
+        if (slot == 0) has_partial0 = true;
         const int pages = (len + ps - 1) >> p.page_log2;
         const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
         const int count = list ? min(p.n_sel, pages) : pages;
@@ -401,6 +414,20 @@ __global__ void __launch_bounds__(kPdThreads, 1)
             }
           }
         }
+        if (slot == 1) {
+          has_meta = true;
+          const long long x = base + tile_weight<NC>(p, sh->w, len, tiles - 1);  // where its last tile begins
+          // the CTA whose piece holds x: the largest j with piece_begin(j) <= x
+          int lo = cta, hi = kPagedCtas - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (piece_begin(total, mid) <= x)
+              lo = mid;
+            else
+              hi = mid - 1;
+          }
+          if (pw == 0 && lane == 0) p.meta[cta] = make_int4(b, hk, lo, 0);
+        }
       }
       base += unit;
       if (++hk == p.hkv) {
@@ -417,11 +444,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       }
     }
     if (pw == 0 && lane == 0 && !has_meta) p.meta[cta] = make_int4(-1, 0, 0, 0);
-    if (pw == 0 && !has_partial0 && lane < G) {  // no piece of an earlier CTA's sequence here
-      float* part = p.partials + (static_cast<long long>(cta) * 2 * 8 + lane) * (D + 2);
-      part[D] = -INFINITY;
-      part[D + 1] = 0.f;
-    }
+    if (pw == 0 && !has_partial0 && lane < G)  // no piece of an earlier CTA's sequence here
+      p.sums[cta * 16 + lane] = make_float2(-INFINITY, 0.f);
     if (!ok && lane == 0) {  // wait (bounded) for this warp's copies in flight
       for (int j = it > NSTG ? it - NSTG : 0; j < it; ++j) {
         if (j % kPdProducers != pw) continue;
@@ -460,7 +484,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     if (lane == 0) mbar_arrive(&sh->join[which]);
     return warp_wait(&sh->join[which], joins & 1, &sh->abort, p.err, 0x504);
   };
-  for (int it = 0;; ++it) {
+  for (int turn = 0;; turn = turn + 1 == kPdGroups ? 0 : turn + 1) {
     const int st = ring.st;
     if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x503)) return;
     ring.next();
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
       for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     }
-    if ((it & 1) == group) {
+    if (turn == group) {
       const int2 my = info->box[bx];
       const int live = my.y - off;                      // live keys from this warp's first on
       const int far = info->len - 1 - (my.x + off);  // distance of its first key
@@ -567,95 +591,126 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sO[(warp * 8 + 2 * kcol + (e & 1)) * C::OROW + 16 * u + krow + (e & 2) * 4] = o[u][e];
     if (!meet(0)) return;
-    for (int i = tid; i < G * D; i += kPdConsumers * 32) {
-      const int g = i / D, e = i % D;
-      float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w) M = fmaxf(M, sh->mw[w][g]);
-      float acc = 0.f, sum = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w) {
-        const float f = M == -INFINITY ? 0.f : ex2_approx(sh->mw[w][g] - M);
-        acc += sO[(w * 8 + g) * C::OROW + e] * f;
-        sum += sh->lw[w][g] * f;
-      }
-      const long long row = static_cast<long long>(b) * p.hq + hk * G + g;
-      if (slot < 0) {
-        static_cast<__nv_bfloat16*>(p.out)[row * D + e] = __float2bfloat16(M == -INFINITY ? 0.f : acc / sum);
-        if (p.lse && e == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kLn2;
-      } else {
-        float* part = p.partials + ((static_cast<long long>(cta) * 2 + slot) * 8 + g) * (D + 2);
-        part[e] = acc;
-        if (e == 0) {
-          part[D] = M;
-          part[D + 1] = sum;
-        }
-      }
+      for (int w = 0; w < kPdConsumers; ++w) top = fmaxf(top, sh->mw[w][2 * kcol + e]);
+      const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - top);
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) sO[(warp * 8 + 2 * kcol + e) * C::OROW + 16 * u + krow + k * 4] = o[u][k + e] * f;
+    }
+    if (tid < 8) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPdConsumers; ++w) top = fmaxf(top, sh->mw[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kPdConsumers; ++w)
+        sum += sh->mw[w][tid] == -INFINITY ? 0.f : sh->lw[w][tid] * ex2_approx(sh->mw[w][tid] - top);
+      sh->m[tid] = top;
+      sh->l[tid] = sum;
     }
     if (!meet(1)) return;
+    for (int i = tid; i < G * (D / 4); i += kPdConsumers * 32) {
+      const int g = i / (D / 4), e = i % (D / 4) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kPdConsumers; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&sO[(w * 8 + g) * C::OROW + e]);
+        acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+      }
+      const float top = sh->m[g], sum = sh->l[g];
+      if (slot < 0) {
+        const long long row = static_cast<long long>(b) * p.hq + hk * G + g;
+        const float r = top == -INFINITY ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + e) =
+            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+        if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+      } else {
+        const int at = (cta * 2 + slot) * 8 + g;
+        *reinterpret_cast<float4*>(p.partials + static_cast<long long>(at) * D + e) = acc;
+        if (e == 0) p.sums[at] = make_float2(top, sum);
+      }
+    }
+    // the next join's writes come behind its first meeting, or of what no one reads any more
     ++joins;
   }
 }
 
 // Joins the pieces of the sequence and head that CTA blockIdx.x began and did not
 // end: its slot 1 and slot 0 of the CTAs up to meta.z.  blockIdx.y = query head.
-// The scales of all pieces are found first, side by side, so that the sums over
-// them wait for no load twice.
+// Two loads deep: maxima and sums of all pieces that there could be are fetched with
+// meta, and the first kAhead rounds of partial sums before the maxima are joined.
+constexpr int kCombineThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(2 * D) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
-  __shared__ float s_f[kPagedCtas], s_red[2 * D / 32], s_acc[D], s_sum[2 * D / 32];
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int kRow = D / 4, kSide = kCombineThreads / kRow;  // threads of a piece, pieces side by side
+  constexpr int kAhead = 5, kWarps = kCombineThreads / 32;
+  static_assert(kPagedCtas <= kCombineThreads, "a piece a thread");
+  __shared__ float s_f[kPagedCtas], s_max[kWarps], s_sum[kWarps];
+  __shared__ float4 s_acc[kCombineThreads];
+  const int tid = threadIdx.x, g = blockIdx.y, first = blockIdx.x, G = p.hq / p.hkv;
+  pdl_launch_dependents();
   pdl_wait();
-  const int4 meta = p.meta[blockIdx.x];
+  const int4 meta = p.meta[first];
+  auto row_of = [&](int i) { return ((first + i) * 2 + (i == 0)) * 8 + g; };
+  float2 own = first + tid < kPagedCtas ? p.sums[row_of(tid)] : make_float2(-INFINITY, 0.f);
   if (meta.x < 0) return;
-  const int G = p.hq / p.hkv, g = blockIdx.y, tid = threadIdx.x;
-  const int first = blockIdx.x, n = meta.z - first + 1;
-  auto part = [&](int i) { return p.partials + ((static_cast<long long>(first + i) * 2 + (i == 0)) * 8 + g) * (D + 2); };
-  constexpr int kPer = (kPagedCtas + 2 * D - 1) / (2 * D);
-  float mi[kPer], li[kPer], M = -INFINITY;
+  const int n = meta.z - first + 1;
+  if (tid >= n) own = make_float2(-INFINITY, 0.f);
+  const int side = tid / kRow, e = tid % kRow * 4;
+  auto part = [&](int i) { return *reinterpret_cast<const float4*>(p.partials + static_cast<long long>(row_of(i)) * D + e); };
+  float4 x[kAhead];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = tid + k * 2 * D;
-    mi[k] = i < n ? part(i)[D] : -INFINITY;
-    li[k] = i < n ? part(i)[D + 1] : 0.f;
-    M = fmaxf(M, mi[k]);
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = side + k * kSide;
+    x[k] = i < n ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float top = own.x;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if ((tid & 31) == 0) s_max[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 2 * D / 32; ++w) M = fmaxf(M, s_red[w]);
-  float l = 0.f;
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w]);
+  const float f = own.x == -INFINITY ? 0.f : ex2_approx(own.x - top);
+  if (tid < n) s_f[tid] = f;
+  float sum = own.y * f;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = tid + k * 2 * D;
-    const float f = mi[k] == -INFINITY ? 0.f : ex2_approx(mi[k] - M);
-    if (i < n) s_f[i] = f;
-    l += li[k] * f;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  if ((tid & 31) == 0) s_sum[tid >> 5] = l;
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
   __syncthreads();
-  l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int i, const float4& v) {
+    const float w = s_f[i];
+    if (w > 0.f) acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;  // an empty piece holds no sums
+  };
 #pragma unroll
-  for (int w = 0; w < 2 * D / 32; ++w) l += s_sum[w];
-  // two halves of the block take every other piece
-  const int e = tid % D;
-  float a = 0.f;
-#pragma unroll 8
-  for (int i = tid / D; i < n; i += 2) {
-    const float f = s_f[i];
-    const float x = f > 0.f ? part(i)[e] : 0.f;  // an empty piece holds no sums
-    a += x * f;
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = side + k * kSide;
+    if (i < n) add(i, x[k]);
   }
-  if (tid >= D) s_acc[e] = a;
+#pragma unroll 4
+  for (int i = side + kAhead * kSide; i < n; i += kSide) add(i, part(i));
+  s_acc[tid] = acc;
   __syncthreads();
-  if (tid >= D) return;
-  a += s_acc[e];
+  if (tid >= kRow) return;
+#pragma unroll
+  for (int k = 1; k < kSide; ++k) {
+    const float4 v = s_acc[tid + k * kRow];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+  }
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
   const long long row = static_cast<long long>(meta.x) * p.hq + meta.y * G + g;
-  static_cast<__nv_bfloat16*>(p.out)[row * D + e] = __float2bfloat16(M == -INFINITY ? 0.f : a / l);
-  if (p.lse && e == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kLn2;
+  const float r = top == -INFINITY ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + e) =
+      make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+  if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int D>
@@ -674,7 +729,7 @@ static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, 
   }
   e = launch_pdl(kern, kPagedCtas, kPdThreads, bytes, s, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_combine_kernel<D>, dim3(kPagedCtas, p.hq / p.hkv), 2 * D, 0, s, p);
+  return launch_pdl(paged_combine_kernel<D>, dim3(kPagedCtas, p.hq / p.hkv), kCombineThreads, 0, s, p);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {

@@ -178,12 +178,12 @@ class Walk:
 
     def at(self, n, x):
         lo, hi = 0, self.tiles(n)
-        while lo < hi:
-            mid = (lo + hi) // 2
-            if self.weight(n, mid) >= x:
-                hi = mid
-            else:
-                lo = mid + 1
+        while lo < hi:  # 32 points at a time, one of them at or above the answer
+            step = (hi - lo + 32) // 32
+            points = [min(hi, lo + lane * step + step - 1) for lane in range(32)]
+            first = next(i for i, t in enumerate(points) if t >= hi or self.weight(n, t) >= x)
+            lo, hi = lo + first * step, min(hi, lo + first * step + step - 1)
+        assert self.weight(n, lo) >= x and (lo == 0 or self.weight(n, lo - 1) < x)
         return lo
 
     def run(self):
