@@ -24,7 +24,9 @@
 // every fourth tile each; a lane looks up the page of one box of 32, a group of
 // boxes ahead (one producer warp that looked pages up tile by tile held the ring
 // empty: 1090 us against 941 for four sequences of 1048576 keys, 28 query and 4 kv
-// heads).  Two groups of four consumer warps take the tiles in turn, 16 keys a warp.
+// heads).  Two groups of four consumer warps take the tiles in turn, 16 keys a warp; at
+// the end of a piece they leave their states to four warps that join them and write,
+// and go on (joined by the consumers themselves a piece cost 1.7 us).
 // Keys are the M rows and query heads (up to 8) the N columns of the warp-level
 // MMAs, S^T = K~ Q~^T and O^T += V^T P^T, so no row of them is padding; P^T
 // goes from accumulators to operand by a register transpose (movmatrix).  P is
@@ -44,7 +46,8 @@ namespace {
 constexpr int kPdGroups = 2;  // of four warps, 16 keys of a tile apiece
 constexpr int kPdConsumers = 4 * kPdGroups;
 constexpr int kPdProducers = 4;  // warps that fill the ring, every fourth tile each
-constexpr int kPdThreads = (kPdConsumers + kPdProducers) * 32;
+constexpr int kPdJoiners = 4;    // warps that join the consumers' states at the end of a piece
+constexpr int kPdThreads = (kPdConsumers + kPdProducers + kPdJoiners) * 32;
 constexpr int kTileKeys = kPagedTileKeys;
 constexpr int kTileLog2 = 6;
 static_assert(1 << kTileLog2 == kTileKeys, "tile");
@@ -77,15 +80,15 @@ constexpr int kFirst = 1, kLast = 2, kEnd = 4;
 template <int D>
 struct PdShared {
   uint64_t full[PdCfg<D>::NSTG], empty[PdCfg<D>::NSTG];
-  uint64_t join[2];  // the consumer warps meet before and after their states are joined
+  uint64_t left, joined;  // the consumers have left their states; the joiners are done with them
   StageInfo info[PdCfg<D>::NSTG];
   int w[kMaxPairs];
   int abort;
   long long scan[kPdThreads / 32];
   int start_b, start_len;  // the sequence that this CTA's piece begins in (-1: no piece)
   long long start_base;
-  float mw[kPdConsumers][8], lw[kPdConsumers][8];  // maxima and row sums of the warps
-  float m[8], l[8];                                // and of all, joined
+  float mw[kPdConsumers][8], lw[kPdConsumers][8];  // maxima and row sums that the consumers have left
+  int left_b, left_hk, left_slot;                  // and of what (left_b -1: that was the last)
 };
 
 template <int D>
@@ -123,23 +126,28 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeParams& p, int len) {
 // live key chunks.  Chunk c is out of reach of the whole tiles before (len - W -
 // 1) / 64, W the window of its last pair.  A list of pages weighs full rows.
 template <int NC>
-__device__ __forceinline__ int tile_weight(const PagedDecodeParams& p, const int* w, int len, int t) {
-  int x = 2 * NC * t;
-  if (!p.selected) {
+struct TileWeight {
+  int dead[NC];
+  __device__ __forceinline__ TileWeight(const PagedDecodeParams& p, const int* w, int len) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) x -= min(t, max(0, (len - w[8 * c + 7] - 1) / kTileKeys));
+    for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, len - w[8 * c + 7] - 1) >> kTileLog2;
   }
-  return x;
-}
+  __device__ __forceinline__ int operator()(int t) const {
+    int x = 2 * NC * t;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) x -= min(t, dead[c]);
+    return x;
+  }
+};
 
-// Smallest t in [0, tiles] with tile_weight(t) >= x, by a warp: 32 points at a time.
+// Smallest t in [0, tiles] with weight(t) >= x, by a warp: 32 points at a time.
 template <int NC>
-__device__ __forceinline__ int tile_at(const PagedDecodeParams& p, const int* w, int len, int tiles, int x) {
+__device__ __forceinline__ int tile_at(const TileWeight<NC>& weight, int tiles, int x) {
   int lo = 0, hi = tiles;
   while (lo < hi) {
     const int step = (hi - lo + 32) >> 5;  // hi is a candidate too
     const int t = min(hi, lo + static_cast<int>(threadIdx.x & 31) * step + step - 1);
-    const int first = __ffs(__ballot_sync(0xffffffffu, t >= hi || tile_weight<NC>(p, w, len, t) >= x)) - 1;
+    const int first = __ffs(__ballot_sync(0xffffffffu, t >= hi || weight(t) >= x)) - 1;
     lo += first * step;
     hi = min(hi, lo + step - 1);
   }
@@ -220,8 +228,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], kPdConsumers);
     }
-    mbar_init(&sh->join[0], kPdConsumers);
-    mbar_init(&sh->join[1], kPdConsumers);
+    mbar_init(&sh->left, kPdConsumers);
+    mbar_init(&sh->joined, kPdJoiners);
     sh->abort = 0;
     sh->start_b = -1;
     fence_mbar_init();
@@ -238,17 +246,16 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   const bool alone = p.batch <= 32 * kPerLane;
   long long total = 0, base = 0;  // weight of all, and before the piece's first sequence
   int b = -1, len = 0;            // the piece's first sequence (-1: no piece)
-  auto weight_of = [&](int n) { return static_cast<long long>(tile_weight<NC>(p, sh->w, n, tiles_of(p, n))) * p.hkv; };
-  auto scan = [&](long long x) {  // inclusive, over the warp
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
+  auto weight_of = [&](int n) { return static_cast<long long>(TileWeight<NC>(p, sh->w, n)(tiles_of(p, n))) * p.hkv; };
+  auto scan = [&](long long x, int lanes) {  // inclusive, over the warp's first lanes
+    for (int off = 1; off < lanes; off <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += o;
     }
     return x;
   };
   if (alone) {
-    if (warp >= kPdConsumers) {
+    if (warp >= kPdConsumers && warp < kPdConsumers + kPdProducers) {
       int n[kPerLane];
       long long x[kPerLane], mine = 0;
       const int per = (p.batch + 31) >> 5;
@@ -256,8 +263,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       for (int j = 0; j < kPerLane; ++j) n[j] = j < per && lane * per + j < p.batch ? clamped_len(p, lane * per + j) : -1;
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) mine += x[j] = n[j] >= 0 ? weight_of(n[j]) : 0;
-      const long long incl = scan(mine);
-      total = __shfl_sync(0xffffffffu, incl, 31);
+      const long long incl = scan(mine, min(p.batch, 32));
+      total = __shfl_sync(0xffffffffu, incl, min(p.batch, 32) - 1);
       const long long from = piece_begin(total, cta);
       long long at = incl - mine;
       const unsigned holds = __ballot_sync(0xffffffffu, from < piece_begin(total, cta + 1) && from >= at && from < incl);
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
     long long mine = 0;
     for (int i = b0; i < b1; ++i) mine += weight_of(clamped_len(p, i));
-    const long long incl = scan(mine);
+    const long long incl = scan(mine, 32);
     if (lane == 31) sh->scan[warp] = incl;
     __syncthreads();
     long long at = incl - mine;
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     base = sh->start_base;
   }
 
-  if (warp >= kPdConsumers) {
+  if (warp >= kPdConsumers && warp < kPdConsumers + kPdProducers) {
     // ================================================================ producer
     RingPos<NSTG> ring;
     const int pw = warp - kPdConsumers;
@@ -318,10 +325,11 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     bool more = b >= 0;
     while (more && ok) {
       const int tiles = tiles_of(p, len);
-      const int unit = tile_weight<NC>(p, sh->w, len, tiles);
+      const TileWeight<NC> weight(p, sh->w, len);
+      const int unit = weight(tiles);
       while (from >= base + unit) base += unit, ++hk;  // heads before the piece, at its beginning only
-      const int t0 = from > base ? tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(from - base)) : 0;
-      const int t1 = to >= base + unit ? tiles : tile_at<NC>(p, sh->w, len, tiles, static_cast<int>(to - base));
+      const int t0 = from > base ? tile_at<NC>(weight, tiles, static_cast<int>(from - base)) : 0;
+      const int t1 = to >= base + unit ? tiles : tile_at<NC>(weight, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
         const int slot = t0 > 0 ? 0 : t1 < tiles ? 1 : -1;
         if (slot == 0) has_partial0 = true;
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
         }
         if (slot == 1) {
           has_meta = true;
-          const long long x = base + tile_weight<NC>(p, sh->w, len, tiles - 1);  // where its last tile begins
+          const long long x = base + weight(tiles - 1);  // where its last tile begins
           // the CTA whose piece holds x: the largest j with piece_begin(j) <= x
           int lo = cta, hi = kPagedCtas - 1;
           while (lo < hi) {
@@ -457,6 +465,42 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     return;
   }
 
+  if (warp >= kPdConsumers) {
+    // ================================================================ joiners
+    for (int k = 0;; ++k) {
+      if (!warp_wait(&sh->left, k & 1, &sh->abort, p.err, 0x504)) return;
+      const int b = sh->left_b, hk = sh->left_hk, slot = sh->left_slot;
+      if (b < 0) return;
+      for (int i = tid - (kPdConsumers + kPdProducers) * 32; i < G * (D / 4); i += kPdJoiners * 32) {
+        const int g = i / (D / 4), e = i % (D / 4) * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPdConsumers; ++w) top = fmaxf(top, sh->mw[w][g]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kPdConsumers; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(&sO[(w * 8 + g) * C::OROW + e]);
+          const float f = top == -INFINITY ? 0.f : ex2_approx(sh->mw[w][g] - top);
+          acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
+          sum += sh->lw[w][g] * f;
+        }
+        if (slot < 0) {
+          const long long row = static_cast<long long>(b) * p.hq + hk * G + g;
+          const float r = top == -INFINITY ? 0.f : 1.f / sum;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + e) =
+              make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+          if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+        } else {
+          const int at = (cta * 2 + slot) * 8 + g;
+          *reinterpret_cast<float4*>(p.partials + static_cast<long long>(at) * D + e) = acc;
+          if (e == 0) p.sums[at] = make_float2(top, sum);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->joined);
+    }
+  }
+
   // ================================================================ consumers
   const float scale = kLog2e * rsqrtf(static_cast<float>(D));
   const int kcol = lane & 3, krow = lane >> 2;  // this lane's pair in a half chunk / head pair, and key row / dim row
@@ -476,13 +520,15 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2*kcol, 2*kcol + 1
   float o[D / 16][4];  // O^T: dims 16u + krow (+8), heads 2*kcol (+1)
   const int w_first = lane < NC ? sh->w[8 * lane] : 0x7fffffff;  // smallest window of chunk `lane`
-  int joins = 0;
+  int pieces = 0;
   RingPos<NSTG> ring;
-  // a bounded wait, so that a warp that gave up does not hold the others
-  auto meet = [&](int which) {
+  // the joiners are done with the last piece's states (a bounded wait)
+  auto joined = [&] { return pieces == 0 || warp_wait(&sh->joined, (pieces - 1) & 1, &sh->abort, p.err, 0x505); };
+  auto leave = [&](int b, int hk, int slot) {
+    if (tid == 0) sh->left_b = b, sh->left_hk = hk, sh->left_slot = slot;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->join[which]);
-    return warp_wait(&sh->join[which], joins & 1, &sh->abort, p.err, 0x504);
+    if (lane == 0) mbar_arrive(&sh->left);
+    ++pieces;
   };
   for (int turn = 0;; turn = turn + 1 == kPdGroups ? 0 : turn + 1) {
     const int st = ring.st;
@@ -490,7 +536,10 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     ring.next();
     const StageInfo* info = &sh->info[st];
     const int flags = info->flags;
-    if (flags & kEnd) return;
+    if (flags & kEnd) {
+      if (joined()) leave(-1, 0, 0);
+      return;
+    }
     if (flags & kFirst) {
       const uint8_t* q = sQ + st * C::Q + krow * (D * 2) + kcol * 4;
 #pragma unroll
@@ -576,66 +625,24 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     if (lane == 0) mbar_arrive(&sh->empty[st]);
     if (!(flags & kLast)) continue;
 
-    // ---- join the warps
+    // ---- the warp's state to the joiners
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int sh_ = 4; sh_ < 32; sh_ <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh_);
+    if (!joined()) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       if (krow == 0) {
         sh->mw[warp][2 * kcol + e] = m[e];
         sh->lw[warp][2 * kcol + e] = l[e];
       }
-    }
-#pragma unroll
-    for (int u = 0; u < D / 16; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sO[(warp * 8 + 2 * kcol + (e & 1)) * C::OROW + 16 * u + krow + (e & 2) * 4] = o[u][e];
-    if (!meet(0)) return;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w) top = fmaxf(top, sh->mw[w][2 * kcol + e]);
-      const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - top);
 #pragma unroll
       for (int u = 0; u < D / 16; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) sO[(warp * 8 + 2 * kcol + e) * C::OROW + 16 * u + krow + k * 4] = o[u][k + e] * f;
+        for (int k = 0; k < 4; k += 2) sO[(warp * 8 + 2 * kcol + e) * C::OROW + 16 * u + krow + k * 4] = o[u][k + e];
     }
-    if (tid < 8) {
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w) top = fmaxf(top, sh->mw[w][tid]);
-#pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w)
-        sum += sh->mw[w][tid] == -INFINITY ? 0.f : sh->lw[w][tid] * ex2_approx(sh->mw[w][tid] - top);
-      sh->m[tid] = top;
-      sh->l[tid] = sum;
-    }
-    if (!meet(1)) return;
-    for (int i = tid; i < G * (D / 4); i += kPdConsumers * 32) {
-      const int g = i / (D / 4), e = i % (D / 4) * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kPdConsumers; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(&sO[(w * 8 + g) * C::OROW + e]);
-        acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
-      }
-      const float top = sh->m[g], sum = sh->l[g];
-      if (slot < 0) {
-        const long long row = static_cast<long long>(b) * p.hq + hk * G + g;
-        const float r = top == -INFINITY ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + e) =
-            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
-        if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
-      } else {
-        const int at = (cta * 2 + slot) * 8 + g;
-        *reinterpret_cast<float4*>(p.partials + static_cast<long long>(at) * D + e) = acc;
-        if (e == 0) p.sums[at] = make_float2(top, sum);
-      }
-    }
-    // the next join's writes come behind its first meeting, or of what no one reads any more
-    ++joins;
+    leave(b, hk, slot);
   }
 }
 
