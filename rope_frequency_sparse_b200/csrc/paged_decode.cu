@@ -51,6 +51,11 @@ constexpr int kPdThreads = (kPdConsumers + kPdProducers + kPdJoiners) * 32;
 constexpr int kTileKeys = kPagedTileKeys;
 constexpr int kTileLog2 = 6;
 static_assert(1 << kTileLog2 == kTileKeys, "tile");
+// What a tile and a sequence's head cost beside their bytes, in 32-byte reads a key.
+// Measured in two batches (28 query and 4 kv heads of 128): without them four
+// sequences of 1048576 keys take 945 us, their near tiles being larger, and 64 of
+// up to 8192 86 us, some CTAs holding ten of them; with them 893 and 83.
+constexpr int kTileCost = 16, kPieceCost = 64;
 constexpr int kPerLane = 4;  // sequences that a lane sums in a small batch
 constexpr int kMaxTilePages = 4;  // boxes of 16 keys
 constexpr float kLog2e = 1.4426950408889634f;
@@ -123,7 +128,7 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeParams& p, int len) {
 }
 
 // Weight of tiles [0, t) of a sequence in 32-byte reads a key: value row plus
-// live key chunks.  Chunk c is out of reach of the whole tiles before (len - W -
+// live key chunks, and the costs above.  Chunk c is out of reach of the whole tiles before (len - W -
 // 1) / 64, W the window of its last pair.  A list of pages weighs full rows.
 template <int NC>
 struct TileWeight {
@@ -133,10 +138,10 @@ struct TileWeight {
     for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, len - w[8 * c + 7] - 1) >> kTileLog2;
   }
   __device__ __forceinline__ int operator()(int t) const {
-    int x = 2 * NC * t;
+    int x = (2 * NC + kTileCost) * t;
 #pragma unroll
     for (int c = 0; c < NC; ++c) x -= min(t, dead[c]);
-    return x;
+    return t > 0 ? x + kPieceCost : 0;
   }
 };
 

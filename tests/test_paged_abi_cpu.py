@@ -152,7 +152,7 @@ def test_bindings_refuse_wrong_tensors():
 
 # ------------------------------------------------------------------ the decode's division of its work
 
-CTAS, TILE = 148, 64
+CTAS, TILE, TILE_COST, PIECE_COST = 148, 64, 16, 64
 
 
 def _cdiv0(a, b):  # C's division, towards zero
@@ -171,7 +171,7 @@ class Walk:
         return max(1, -(-keys // TILE))
 
     def weight(self, n, t):
-        x = 2 * self.nc * t
+        x = (2 * self.nc + TILE_COST) * t + (PIECE_COST if t else 0)
         if self.n_sel is None:
             x -= sum(min(t, max(0, _cdiv0(n - self.w[8 * c + 7] - 1, TILE))) for c in range(self.nc))
         return x
@@ -255,7 +255,7 @@ def test_tile_weights_count_the_live_chunks():
         for t in range(walk.tiles(n)):
             near = n - 1 - (min(n, (t + 1) * TILE) - 1)
             live = sum(1 for c in range(d // 16) if near <= walk.w[8 * c + 7])
-            assert walk.weight(n, t + 1) - walk.weight(n, t) == d // 16 + live
+            assert walk.weight(n, t + 1) - walk.weight(n, t) == d // 16 + live + TILE_COST + (0 if t else PIECE_COST)
 
 
 @pytest.mark.parametrize("seed", range(30))
