@@ -334,32 +334,31 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       const int unit = weight(tiles);
       while (from >= base + unit) base += unit, ++hk;  // heads before the piece, at its beginning only
       const int t0 = from > base ? tile_at<NC>(weight, tiles, static_cast<int>(from - base)) : 0;
+      const int pages = (len + ps - 1) >> p.page_log2;
+      const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
+      const int count = list ? min(p.n_sel, pages) : pages;
+      const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+      // 32 boxes at a time, a lane each (under way before t1 is looked for): of the group in use the page in the
+      // sequence (-1: none) and in the pool, and, on their way, the next group's
+      // entries of the table and the list entries of the one after it
+      auto listed = [&](int i) {  // page of box i in the sequence
+        const int k = i >> sub_log2;
+        return k < count ? (list ? list[k] : k) : -1;
+      };
+      auto in_pool = [&](int& logical) {  // its page in the pool, not yet looked at
+        if (logical >= pages) {
+          atomicCAS(p.err, 0u, kErrBadSelect);
+          logical = -1;
+        }
+        return logical >= 0 ? table[logical] : 0;
+      };
+      int logical_next = listed(t0 * boxes + lane);
+      int page_next = in_pool(logical_next);
+      int logical_far = listed(t0 * boxes + 32 + lane);
       const int t1 = to >= base + unit ? tiles : tile_at<NC>(weight, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
         const int slot = t0 > 0 ? 0 : t1 < tiles ? 1 : -1;
         if (slot == 0) has_partial0 = true;
-        const int pages = (len + ps - 1) >> p.page_log2;
-        const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
-        const int count = list ? min(p.n_sel, pages) : pages;
-        const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
-        // 32 boxes at a time, a lane each: of the group in use the page in the
-        // sequence (-1: none) and in the pool, and, on their way, the next group's
-        // entries of the table and the list entries of the one after it
-        const int end = t1 * boxes;
-        auto listed = [&](int i) {  // page of box i in the sequence
-          const int k = i >> sub_log2;
-          return i < end && k < count ? (list ? list[k] : k) : -1;
-        };
-        auto in_pool = [&](int& logical) {  // its page in the pool, not yet looked at
-          if (logical >= pages) {
-            atomicCAS(p.err, 0u, kErrBadSelect);
-            logical = -1;
-          }
-          return logical >= 0 ? table[logical] : 0;
-        };
-        int logical_next = listed(t0 * boxes + lane);
-        int page_next = in_pool(logical_next);
-        int logical_far = listed(t0 * boxes + 32 + lane);
         for (int tg = t0; tg < t1 && ok; tg += 32 >> (kTileLog2 - box_log2)) {
           // this lane's box of the group
           const int i = tg * boxes + lane;
