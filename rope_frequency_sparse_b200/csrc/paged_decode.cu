@@ -59,6 +59,7 @@ constexpr int kTileCost = 16, kPieceCost = 64;
 constexpr int kPerLane = 4;  // sequences that a lane sums in a small batch
 constexpr int kMaxTilePages = 4;  // boxes of 16 keys
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -72,15 +73,13 @@ struct PdCfg {
   static constexpr int MERGE = kPdConsumers * 8 * OROW * 4;
 };
 
-struct StageInfo {
+struct __align__(16) StageInfo {
+  int4 tile;                // keys of the sequence; first chunk loaded | flags | slot + 1; sequence; kv head
   int2 box[kMaxTilePages];  // first key of each box of the tile, and its live keys (0: no such page)
-  int len;                  // keys of the sequence
-  int clo;                  // first chunk loaded
-  int flags;                // kFirst, kLast, kEnd
-  int slot;                 // partial slot of the CTA, -1: the whole sequence, write the output
-  int b, hk;
 };
-constexpr int kFirst = 1, kLast = 2, kEnd = 4;
+// In tile.y: bits 0-7 the first chunk loaded, 8-10 these flags, 16-17 one more than the
+// CTA's partial slot (0: the whole sequence, write the output).
+constexpr int kFirst = 0x100, kLast = 0x200, kEnd = 0x400;
 
 template <int D>
 struct PdShared {
@@ -398,12 +397,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
             if (tile == t) {
               info->box[lane & (boxes - 1)] = make_int2(key0, keys);
               if (lead) {
-                info->len = len;
-                info->clo = clo;
-                info->flags = (t == t0 ? kFirst : 0) | (t + 1 == t1 ? kLast : 0);
-                info->slot = slot;
-                info->b = b;
-                info->hk = hk;
+                info->tile = make_int4(len, clo | (t == t0 ? kFirst : 0) | (t + 1 == t1 ? kLast : 0) | (slot + 1) << 16, b, hk);
               }
             }
             __syncwarp();
@@ -451,7 +445,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     if (ok && it % kPdProducers == pw) {  // the end mark
       if (it >= NSTG) ok = warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x502);
       if (ok && lane == 0) {
-        sh->info[ring.st].flags = kEnd;
+        sh->info[ring.st].tile.y = kEnd;
         mbar_arrive(&sh->full[ring.st]);
       }
     }
@@ -538,8 +532,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     const int st = ring.st;
     if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x503)) return;
     ring.next();
-    const StageInfo* info = &sh->info[st];
-    const int flags = info->flags;
+    const int4 tile = sh->info[st].tile;
+    const int2 my = sh->info[st].box[bx];
+    const int flags = tile.y;
     if (flags & kEnd) {
       if (joined()) leave(-1, 0, 0);
       return;
@@ -556,15 +551,14 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     }
     if (turn == group) {
-      const int2 my = info->box[bx];
-      const int live = my.y - off;                      // live keys from this warp's first on
-      const int far = info->len - 1 - (my.x + off);  // distance of its first key
+      const int live = my.y - off;                  // live keys from this warp's first on
+      const int far = tile.x - 1 - (my.x + off);  // distance of its first key
       const uint32_t stg = smem_u32(sStage + st * C::STAGE);
 
       // ---- S^T of 16 keys, pairs beyond their window zeroed
       const int dirty = __popc(__ballot_sync(0xffffffffu, far > w_first));
       float s[4] = {0.f, 0.f, 0.f, 0.f};
-      qk_from<NC, 0>(info->clo, s, stg + k_at, cbytes, k_odd, qf, dirty, far, sh->w, krow, kcol);
+      qk_from<NC, 0>(flags & 0xff, s, stg + k_at, cbytes, k_odd, qf, dirty, far, sh->w, krow, kcol);
       // the values' first half is fetched while the softmax runs
       uint32_t va[D / 32][4];
       auto load_v = [&](int u0) {
@@ -575,22 +569,23 @@ __global__ void __launch_bounds__(kPdThreads, 1)
         }
       };
       load_v(0);
-      // ---- online softmax of heads 2*kcol, 2*kcol + 1
-      float mu[2], corr[2];
+      // ---- online softmax of heads 2*kcol, 2*kcol + 1.  The maximum that weights are
+      // taken against is raised only where a logit is more than kSlack above it: they
+      // stay below 2^kSlack, and most tiles need no reduction over the warp
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[e] = krow < live ? s[e] * scale : -INFINITY;
-        s[e + 2] = krow + 8 < live ? s[e + 2] * scale : -INFINITY;
-        float mx = fmaxf(s[e], s[e + 2]);
+      for (int e = 0; e < 4; ++e) s[e] = krow + (e & 2) * 4 < live ? s[e] * scale : -INFINITY;
+      if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m[0] + kSlack || fmaxf(s[1], s[3]) > m[1] + kSlack)) {
+        float corr[2];
 #pragma unroll
-        for (int sh_ = 4; sh_ < 32; sh_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh_));
-        const float mn = fmaxf(m[e], mx);
-        mu[e] = mn == -INFINITY ? 0.f : mn;  // no live key yet
-        corr[e] = ex2_approx(m[e] - mu[e]);
-        m[e] = mn;
-        l[e] *= corr[e];
-      }
-      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(s[e], s[e + 2]);
+#pragma unroll
+          for (int sh_ = 4; sh_ < 32; sh_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh_));
+          mx = fmaxf(m[e], mx);
+          corr[e] = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mx);
+          m[e] = mx;
+          l[e] *= corr[e];
+        }
 #pragma unroll
         for (int u = 0; u < D / 16; ++u)
 #pragma unroll
@@ -599,7 +594,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        pr[e] = ex2_approx(s[e] - mu[e & 1]);
+        pr[e] = ex2_approx(s[e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1]));  // no live key yet
         l[e & 1] += pr[e];
       }
       const uint32_t pb0 = movmatrix_t(pack_bf16x2(pr[0], pr[1])), pb1 = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
@@ -624,7 +619,6 @@ __global__ void __launch_bounds__(kPdThreads, 1)
         for (int u = 0; u < D / 32; ++u) mma_bf16_16816(o[half * (D / 32) + u], va[u], pb0, pb1);
       }
     }
-    const int b = info->b, hk = info->hk, slot = info->slot;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->empty[st]);
     if (!(flags & kLast)) continue;
@@ -646,7 +640,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; k += 2) sO[(warp * 8 + 2 * kcol + e) * C::OROW + 16 * u + krow + k * 4] = o[u][k + e];
     }
-    leave(b, hk, slot);
+    leave(tile.z, tile.w, (flags >> 16) - 1);
   }
 }
 
