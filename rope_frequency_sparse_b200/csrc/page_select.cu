@@ -23,8 +23,8 @@
 // pages are that close, or a sum is not finite, every page is scored in fp64.
 //
 // First kernel: bound by the bounds' bytes, 4 d a page and kv head less the pairs
-// that are out of reach.  Second kernel, one CTA per sequence and kv head, bound by
-// its passes over the scores: the order-preserving bit patterns are binned linearly
+// that are out of reach.  Second kernel (it scores short lists itself), one CTA per
+// sequence and kv head, bound by its passes over the scores: the order-preserving bit patterns are binned linearly
 // between the least and the greatest, and the bin of the last kept one again, until
 // few are left; a bin's edges are exact, so any distribution ends (each round parts
 // the least from the greatest).  Where the places are at most a quarter of the groups
@@ -42,10 +42,14 @@ namespace {
 using u64 = unsigned long long;
 
 constexpr int kScoreThreads = 128;
-constexpr int kSelectThreads = 512;  // at most
+constexpr int kSelectThreads = 512;
+// Pages of a list that one CTA scores and selects: eight lists of up to 250 pages take
+// 15.3 us with their decode, 16.5 by two kernels; 32 x 4 of up to 1024 would take 53
+// against 49.
+constexpr int kShort = 512;
 constexpr int kBins = 2048, kBinBits = 11;
 constexpr int kAgain = 256;       // pages that are scored again and ranked one against another
-constexpr int kCandidates = 1024;  // pages that are looked at one by one, of groups with a high score
+constexpr int kCandidates = 4096;  // pages that are looked at one by one, of groups with a high score
 constexpr int kFewPages = 24;     // a bin of at most this many is not binned again: each goes to a warp
 constexpr int kHeld = 4;          // scores that a thread holds in registers at most
 // A step of 16 products is off by at most 18 * 2^-23 of the magnitudes summed so
@@ -100,6 +104,7 @@ struct Scores {
       : key(reinterpret_cast<unsigned*>(p.keys + static_cast<long long>(list) * p.max_pages)),
         size(key + p.max_pages),
         high(size + (p.max_pages + kGroup - 1) / kGroup) {}
+  __device__ Scores(unsigned* key_, unsigned* size_, unsigned* high_) : key(key_), size(size_), high(high_) {}
 };
 
 }  // namespace
@@ -108,19 +113,11 @@ struct Scores {
 // 16-byte pieces 4 j + kcol of the 2 d bounds, and of query head `row` the same
 // pieces: the sum's order of elements is the MMA's to choose.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ PageSelectParams p) {
+__device__ __forceinline__ void score_group(const PageSelectParams& p, int b, int hk, int len, int pages, int group,
+                                            const int* sw, const Scores& out) {
   constexpr int NJ = D / 32;  // pieces of the minima a lane holds, and of the maxima
-  const int tid = threadIdx.x, lane = tid & 31, row = lane >> 2, kcol = lane & 3;
-  const int hk = blockIdx.y % p.hkv, b = blockIdx.y / p.hkv, G = p.hq / p.hkv;
-  __shared__ int sw[kMaxPairs];
-  for (int i = tid; i < kMaxPairs; i += kScoreThreads) sw[i] = p.win.w[i];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int len = select_len(p, b), ps = 1 << p.page_log2;
-  const int pages = (len + ps - 1) >> p.page_log2;
-  if (pages <= p.n_sel || static_cast<long long>(blockIdx.x) * (kScoreThreads / 2) >= pages) return;
-  __syncthreads();
-  const int pg0 = blockIdx.x * (kScoreThreads / 2) + (tid >> 5) * 16 + row;
+  const int lane = threadIdx.x & 31, row = lane >> 2, kcol = lane & 3, G = p.hq / p.hkv;
+  const int pg0 = group * kGroup + row;
   const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
   int page[2];
 #pragma unroll
@@ -172,7 +169,6 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
       mma_bf16_16816(m, fa, y[2 * h] & kAbs, y[2 * h + 1] & kAbs);
     }
   }
-  Scores out(p, b * p.hkv + hk);
   float size = 0.f;   // greatest S of the warp's pages
   unsigned high = 0;  // and greatest score of those that compete for a place
 #pragma unroll
@@ -192,7 +188,22 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
   }
   const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(size));  // in the order of magnitudes
   high = __reduce_max_sync(0xffffffffu, high);
-  if (lane == 0 && pg0 < pages) out.size[pg0 / kGroup] = bits, out.high[pg0 / kGroup] = high;
+  if (lane == 0 && pg0 < pages) out.size[group] = bits, out.high[group] = high;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ PageSelectParams p) {
+  const int hk = blockIdx.y % p.hkv, b = blockIdx.y / p.hkv;
+  __shared__ int sw[kMaxPairs];
+  for (int i = threadIdx.x; i < kMaxPairs; i += kScoreThreads) sw[i] = p.win.w[i];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = select_len(p, b);
+  const int pages = (len + (1 << p.page_log2) - 1) >> p.page_log2;
+  if (pages <= p.n_sel || static_cast<long long>(blockIdx.x) * (kScoreThreads / 2) >= pages) return;
+  __syncthreads();
+  score_group<D>(p, b, hk, len, pages, blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5), sw,
+                 Scores(p, b * p.hkv + hk));
 }
 
 namespace {
@@ -396,10 +407,10 @@ __device__ __forceinline__ void mark_best(SelectShared* sh, const PageSelectPara
 
 }  // namespace
 
+// kScore: short lists, whose pages this kernel scores itself, to shared memory.
 // kMine: scores that a thread holds in registers; 0: more pages than that, the
-// scores are read again from memory by each pass.  Threads: a multiple of 32, 256
-// to kSelectThreads.
-template <int D, int kMine>
+// scores are read again from memory by each pass.  kSelectThreads threads.
+template <int D, int kMine, bool kScore>
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ PageSelectParams p) {
   __shared__ __align__(16) SelectShared s;
   SelectShared* sh = &s;
@@ -411,11 +422,17 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
   const int len = select_len(p, b);
   const int pages = (len + (1 << p.page_log2) - 1) >> p.page_log2;
   u64* keys = p.keys + static_cast<long long>(blockIdx.x) * p.max_pages;  // 64-bit scores, where they are needed
-  const Scores scores(p, blockIdx.x);
+  __shared__ unsigned s_key[kScore ? kShort : 1], s_size[kScore ? kShort / kGroup : 1], s_high[kScore ? kShort / kGroup : 1];
+  const Scores scores = kScore ? Scores(s_key, s_size, s_high) : Scores(p, blockIdx.x);
   int* out = p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel;
   if (pages <= p.n_sel) {
     for (int i = tid; i < p.n_sel; i += T) out[i] = i < pages ? i : -1;
     return;
+  }
+  if constexpr (kScore) {
+    __syncthreads();
+    for (int i = warp; i * kGroup < pages; i += warps) score_group<D>(p, b, hk, len, pages, i, sh->w, scores);
+    __syncthreads();
   }
   // pages [i0, i1) compete for `places`
   const int i0 = p.n_first, i1 = pages - p.n_last, places = p.n_sel - p.n_first - p.n_last;
@@ -471,13 +488,14 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
       __syncthreads();
       const int n = sh->n_groups;
       if (n <= kCandidates / kGroup) {
-        for (int x = tid; x < n * kGroup; x += T) {
-          const int i = sh->groups[x / kGroup] * kGroup + x % kGroup;
+        for (int x0 = 0; x0 < n * kGroup; x0 += T) {
+          const int x = x0 + tid, i = x < n * kGroup ? sh->groups[x / kGroup] * kGroup + x % kGroup : pages;
           const unsigned k = i < pages && !forced(i) ? scores.key[i] : 0;
-          if (k < least) continue;
-          const int at = atomicAdd(&sh->n, 1);
-          sh->key[at] = k;
-          sh->page[at] = i;
+          const unsigned in = __ballot_sync(0xffffffffu, k >= least);  // least is above 0
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh->n, __popc(in));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << lane) - 1));
+          if (k >= least) sh->key[at] = k, sh->page[at] = i;
         }
         __syncthreads();
         const int m = sh->n;
@@ -669,14 +687,14 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
 
 template <int D>
 static cudaError_t launch_select(const PageSelectParams& p, cudaStream_t s) {
+  const int lists = p.batch * p.hkv;
+  if (p.max_pages <= kShort) return launch_pdl(page_select_kernel<D, kHeld, true>, lists, kSelectThreads, 0, s, p);
   const int per = kScoreThreads / 2;
-  const dim3 grid((p.max_pages + per - 1) / per, p.batch * p.hkv);
+  const dim3 grid((p.max_pages + per - 1) / per, lists);
   cudaError_t e = launch_pdl(page_score_kernel<D>, grid, kScoreThreads, 0, s, p);
   if (e != cudaSuccess) return e;
-  const int lists = p.batch * p.hkv;
-  if (p.max_pages > kSelectThreads * kHeld) return launch_pdl(page_select_kernel<D, 0>, lists, kSelectThreads, 0, s, p);
-  const int threads = p.max_pages <= 256 * kHeld ? 256 : (p.max_pages + 32 * kHeld - 1) / (32 * kHeld) * 32;
-  return launch_pdl(page_select_kernel<D, kHeld>, lists, threads, 0, s, p);
+  if (p.max_pages > kSelectThreads * kHeld) return launch_pdl(page_select_kernel<D, 0, false>, lists, kSelectThreads, 0, s, p);
+  return launch_pdl(page_select_kernel<D, kHeld, false>, lists, kSelectThreads, 0, s, p);
 }
 
 cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s) {
