@@ -93,6 +93,7 @@ struct PdShared {
   long long start_base;
   float mw[kPdConsumers][8], lw[kPdConsumers][8];  // maxima and row sums that the consumers have left
   int left_b, left_hk, left_slot;                  // and of what (left_b -1: that was the last)
+  int passed;                                      // stages that the first consumer has passed
 };
 
 template <int D>
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     mbar_init(&sh->left, kPdConsumers);
     mbar_init(&sh->joined, kPdJoiners);
     sh->abort = 0;
+    sh->passed = 0;
     sh->start_b = -1;
     fence_mbar_init();
   }
@@ -466,7 +468,20 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   if (warp >= kPdConsumers) {
     // ================================================================ joiners
     for (int k = 0;; ++k) {
-      if (!warp_wait(&sh->left, k & 1, &sh->abort, p.err, 0x504)) return;
+      // a piece may be as long as the kernel: the limit starts anew with each stage passed
+      bool ok = mbar_try_wait(&sh->left, k & 1);
+      int seen = -1;
+      for (long long t0 = 0; !ok && !*static_cast<volatile int*>(&sh->abort); ok = mbar_try_wait(&sh->left, k & 1)) {
+        const int now = *static_cast<volatile int*>(&sh->passed);
+        if (now != seen) {
+          seen = now;
+          t0 = clock64();
+        } else if (clock64() - t0 > kWaitLimitCycles) {
+          atomicCAS(p.err, 0u, 0x504u);
+          sh->abort = 1;
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) return;
       const int b = sh->left_b, hk = sh->left_hk, slot = sh->left_slot;
       if (b < 0) return;
       for (int i = tid - (kPdConsumers + kPdProducers) * 32; i < G * (D / 4); i += kPdJoiners * 32) {
@@ -518,7 +533,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2*kcol, 2*kcol + 1
   float o[D / 16][4];  // O^T: dims 16u + krow (+8), heads 2*kcol (+1)
   const int w_first = lane < NC ? sh->w[8 * lane] : 0x7fffffff;  // smallest window of chunk `lane`
-  int pieces = 0;
+  int pieces = 0, passed = 0;
   RingPos<NSTG> ring;
   // the joiners are done with the last piece's states (a bounded wait)
   auto joined = [&] { return pieces == 0 || warp_wait(&sh->joined, (pieces - 1) & 1, &sh->abort, p.err, 0x505); };
@@ -535,6 +550,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     const int4 tile = sh->info[st].tile;
     const int2 my = sh->info[st].box[bx];
     const int flags = tile.y;
+    if (tid == 0) *static_cast<volatile int*>(&sh->passed) = ++passed;
     if (flags & kEnd) {
       if (joined()) leave(-1, 0, 0);
       return;

@@ -4,7 +4,7 @@ against the fp64 oracle.
 Tolerances.  A rounding to bf16 is off by at most 2^-8 of the value, to fp32 by 2^-24.
 Norm and rotation run in fp32: the sum of d <= 128 squares is off by at most 2^-17
 relative, half of that after the square root, the other steps by a few 2^-24, the sine
-and cosine of a turn's fraction by 2^-22: together below 2^-16 of |a| + |b| of the
+and cosine of a turn's fraction by 2^-22 (for bf16 rows by 2^-21): together below 2^-16 of |a| + |b| of the
 pair.  The decode rounds each softmax weight to bf16 (2^-8 of the weighted |v|); a
 logit is off by at most 18 * 2^-23 a tensor-core step of the sum of |q k| (the bound
 the FASA scores are held to), which scales a weight by as much, twice (numerator and
@@ -80,7 +80,7 @@ def test_norm_rope_against_oracle(T, Hq, Hkv, d, dtype, pairing, axes, norm):
     for x, w, y in zip((q, k), (wq, wk), got):
         want, size = paged.norm_rope(paged.f64(x), None if w is None else paged.f64(w), eps, pos.cpu().numpy(),
                                      _axes(d, axes), theta, pairing)
-        # positions near 2^31 turn by up to 2^29 turns: the fp64 product is off by 2^-53 of them, 2^-21 of an angle
+        # positions near 2^31 turn by up to 2^29 turns: the oracle's fp64 product is off by 2^-53 of them, 2^-21 of an angle
         _within(y, want, half * np.abs(want) + (2.0 ** -16 + 2.0 ** -20) * size)
 
 
@@ -604,3 +604,23 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     atf.atf_check()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_scratch_and_outputs_of_a_call_on_a_given_stream():
+    """What a call allocates is not handed out again while the other stream still uses it."""
+    theta, alpha = 1e7, 1.0
+    c = _decode_case([40000, 300], 28, 4, 128, 64, theta, alpha, seed=131)
+    bd = torch.sort(_normal(132, c[1].shape[0], 4, 2, 128), dim=2).values
+    want = atf.paged_decode(*c, theta, alpha)
+    sel = atf.page_select(c[0], bd, c[3], c[4], 64, 9, theta, alpha)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        got.append((atf.paged_decode(*c, theta, alpha, stream=side),
+                    atf.page_select(c[0], bd, c[3], c[4], 64, 9, theta, alpha, stream=side.cuda_stream)))
+        for n in (1 << 20, 1 << 17, 1 << 14):  # sizes of the scratch, on the current stream
+            torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    atf.atf_check()
+    assert all(torch.equal(o, want) and torch.equal(s, sel) for o, s in got)
