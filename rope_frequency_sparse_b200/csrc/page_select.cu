@@ -53,9 +53,9 @@ constexpr int kCandidates = 4096;  // pages that are looked at one by one, of gr
 constexpr int kFewPages = 24;     // a bin of at most this many is not binned again: each goes to a warp
 constexpr int kHeld = 4;          // scores that a thread holds in registers at most
 // A step of 16 products is off by at most 18 * 2^-23 of the magnitudes summed so
-// far; 16 steps stay below 2^-14.8, and the rest of 2^-14 covers the roundings of S
-// and of the thresholds.
-constexpr float kEps = 6.103515625e-05f;
+// far; the four steps of a sum stay below 2^-16.8, and the rest of 2^-16 covers the
+// sums' own sum and the roundings of S and of the thresholds.
+constexpr float kEps = 1.52587890625e-05f;
 
 __device__ __forceinline__ int select_len(const PageSelectParams& p, int b) {
   const int len = p.kv_len[b];
@@ -142,7 +142,9 @@ __device__ __forceinline__ void score_group(const PageSelectParams& p, int b, in
       v[r][j] = live && page[r] >= 0 && reach ? bounds[4 * j + kcol] : zero;
     }
   }
-  float a[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+  float a4[4][4], m[4] = {0.f, 0.f, 0.f, 0.f};  // four sums of scores: less error, shorter chains
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a4[i][0] = a4[i][1] = a4[i][2] = a4[i][3] = 0.f;
 #pragma unroll
   for (int j = 0; j < 2 * NJ; ++j) {
     uint32_t x[2][4], y[4];
@@ -163,12 +165,15 @@ __device__ __forceinline__ void score_group(const PageSelectParams& p, int b, in
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t f[4] = {x[0][2 * h], x[1][2 * h], x[0][2 * h + 1], x[1][2 * h + 1]};
-      mma_bf16_16816(a, f, y[2 * h], y[2 * h + 1]);
+      mma_bf16_16816(a4[(2 * j + h) & 3], f, y[2 * h], y[2 * h + 1]);
       constexpr uint32_t kAbs = 0x7FFF7FFFu;
       const uint32_t fa[4] = {f[0] & kAbs, f[1] & kAbs, f[2] & kAbs, f[3] & kAbs};
       mma_bf16_16816(m, fa, y[2 * h] & kAbs, y[2 * h + 1] & kAbs);
     }
   }
+  float a[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = (a4[0][e] + a4[1][e]) + (a4[2][e] + a4[3][e]);
   float size = 0.f;   // greatest S of the warp's pages
   unsigned high = 0;  // and greatest score of those that compete for a place
 #pragma unroll
@@ -192,7 +197,7 @@ __device__ __forceinline__ void score_group(const PageSelectParams& p, int b, in
 }
 
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ PageSelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 5) page_score_kernel(const __grid_constant__ PageSelectParams p) {
   const int hk = blockIdx.y % p.hkv, b = blockIdx.y / p.hkv;
   __shared__ int sw[kMaxPairs];
   for (int i = threadIdx.x; i < kMaxPairs; i += kScoreThreads) sw[i] = p.win.w[i];
@@ -346,20 +351,26 @@ template <int D>
 __device__ __forceinline__ u64 exact_score(const PageSelectParams& p, const int* windows, int b, int hk, int len, int page) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, G = p.hq / p.hkv;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const int entry = pool_page(p, p.page_table[static_cast<long long>(b) * p.max_pages + page]);
-  const int near = page_distance(p, len, page);
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
                                                   (static_cast<long long>(hk) * G + min(g, G - 1)) * D);
+  // every load under way, then a rolled loop over the pieces: this runs for a few pages
+  // a launch, and the fetch of straight-line code took longer than its execution
+  uint4 xs[D / 32], mns[D / 32], mxs[D / 32];
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) xs[j] = q[4 * j + c];
+  const int entry = pool_page(p, p.page_table[static_cast<long long>(b) * p.max_pages + page]);
+  const int near = page_distance(p, len, page);
   const uint4* bounds = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bounds) +
                                                        (static_cast<long long>(max(entry, 0)) * p.hkv + hk) * 2 * D);
-  // a rolled loop, a piece ahead: this runs for a few pages a launch, and the fetch of
-  // straight-line code took longer than its execution
-  uint4 x = q[c], mn = entry >= 0 ? bounds[c] : zero, mx = entry >= 0 ? bounds[D / 8 + c] : zero;
-  double s = 0.0;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    mns[j] = entry >= 0 ? bounds[4 * j + c] : zero;
+    mxs[j] = entry >= 0 ? bounds[D / 8 + 4 * j + c] : zero;
+  }
+  double part[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};  // side by side: a chain of fp64 sums is slow
 #pragma unroll 1
   for (int j = 0; j < D / 32; ++j) {
-    const int next = 4 * min(j + 1, D / 32 - 1) + c;
-    const uint4 x1 = q[next], mn1 = entry >= 0 ? bounds[next] : zero, mx1 = entry >= 0 ? bounds[D / 8 + next] : zero;
+    const uint4 x = xs[j], mn = mns[j], mx = mxs[j];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t w = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
@@ -370,11 +381,11 @@ __device__ __forceinline__ u64 exact_score(const PageSelectParams& p, const int*
       for (int e = 0; e < 2; ++e) {
         const double y = e ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
         const double best = fmax(y * (e ? bf16hi_to_f32(l) : bf16lo_to_f32(l)), y * (e ? bf16hi_to_f32(h) : bf16lo_to_f32(h)));
-        if (on) s += best;
+        part[2 * k + e] += on ? best : 0.0;
       }
     }
-    x = x1, mn = mn1, mx = mx1;
   }
+  double s = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
 #pragma unroll
