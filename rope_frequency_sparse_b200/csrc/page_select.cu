@@ -47,10 +47,10 @@ constexpr int kSelectThreads = 512;
 // 15.3 us with their decode, 16.5 by two kernels; 32 x 4 of up to 1024 would take 53
 // against 49.
 constexpr int kShort = 512;
-constexpr int kBins = 2048, kBinBits = 11;
+constexpr int kBins = 1024, kBinBits = 10;  // eight bins a thread of the smallest block
 constexpr int kAgain = 256;       // pages that are scored again and ranked one against another
 constexpr int kCandidates = 4096;  // pages that are looked at one by one, of groups with a high score
-constexpr int kFewPages = 24;     // a bin of at most this many is not binned again: each goes to a warp
+constexpr int kFewGroups = 24;    // a bin of at most this many groups is not binned again
 constexpr int kHeld = 4;          // scores that a thread holds in registers at most
 // A step of 16 products is off by at most 18 * 2^-23 of the magnitudes summed so
 // far; the four steps of a sum stay below 2^-16.8, and the rest of 2^-16 covers the
@@ -406,12 +406,12 @@ __device__ __forceinline__ void mark_best(SelectShared* sh, const PageSelectPara
     }
     __syncthreads();
   }
-  if (tid < close) {
+  for (int i = tid; i < close; i += blockDim.x) {
     int before = 0;
     if (close > need)
       for (int j = 0; j < close; ++j)
-        before += sh->cand[j] > sh->cand[tid] || (sh->cand[j] == sh->cand[tid] && sh->again[j] < sh->again[tid]);
-    sh->mark[tid] = before < need;
+        before += sh->cand[j] > sh->cand[i] || (sh->cand[j] == sh->cand[i] && sh->again[j] < sh->again[i]);
+    sh->mark[i] = before < need;
   }
   __syncthreads();
 }
@@ -420,7 +420,8 @@ __device__ __forceinline__ void mark_best(SelectShared* sh, const PageSelectPara
 
 // kScore: short lists, whose pages this kernel scores itself, to shared memory.
 // kMine: scores that a thread holds in registers; 0: more pages than that, the
-// scores are read again from memory by each pass.  kSelectThreads threads.
+// scores are read again from memory by each pass.  128 to
+// kSelectThreads threads.
 template <int D, int kMine, bool kScore>
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ PageSelectParams p) {
   __shared__ __align__(16) SelectShared s;
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
     if (slack < INFINITY) {
       const unsigned top = hi;
       int need = places, count = groups;
-      narrow(sh, each_group, lo, hi, need, count, kFewPages);
+      narrow(sh, each_group, lo, hi, need, count, kFewGroups);
       const unsigned least = below(lo, slack);
       each_group([&](int i, unsigned k, int) {
         if (k < least) return;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
         };
         lo = least, need = places, count = m;
         hi = top;
-        narrow(sh, each_candidate, lo, hi, need, count, kFewPages);
+        narrow(sh, each_candidate, lo, hi, need, count, 1);
         const unsigned cut_lo = below(lo, slack), cut_hi = below(hi, -slack);
         __syncthreads();
         if (tid == 0) sh->n = 0;
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
   bool again = !(slack < INFINITY);
   if (!again) {
     int need = places, count = i1 - i0;
-    narrow(sh, each, lo, hi, need, count, kFewPages);
+    narrow(sh, each, lo, hi, need, count, 1);
     const unsigned cut_lo = below(lo, slack), cut_hi = below(hi, -slack);
     int above = 0;
     unsigned bits = 0, unsure = 0;  // this thread's pages that are kept, and that are scored again
@@ -676,8 +677,8 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
       if (k >= lo64 && k <= hi64) sh->cand[atomicAdd(&sh->n, 1)] = k;
     });
     __syncthreads();
-    if (tid < count) {
-      const u64 own = sh->cand[tid];
+    for (int i = tid; i < count; i += T) {
+      const u64 own = sh->cand[i];
       int above = 0, equal = 0;
       for (int j = 0; j < count; ++j) {
         above += sh->cand[j] > own;
@@ -699,7 +700,9 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
 template <int D>
 static cudaError_t launch_select(const PageSelectParams& p, cudaStream_t s) {
   const int lists = p.batch * p.hkv;
-  if (p.max_pages <= kShort) return launch_pdl(page_select_kernel<D, kHeld, true>, lists, kSelectThreads, 0, s, p);
+  // short lists: a warp a group of pages, so that an SM holds several of many lists
+  const int threads = p.max_pages <= 128 ? 128 : p.max_pages <= 256 ? 256 : kSelectThreads;
+  if (p.max_pages <= kShort) return launch_pdl(page_select_kernel<D, kHeld, true>, lists, threads, 0, s, p);
   const int per = kScoreThreads / 2;
   const dim3 grid((p.max_pages + per - 1) / per, lists);
   cudaError_t e = launch_pdl(page_score_kernel<D>, grid, kScoreThreads, 0, s, p);

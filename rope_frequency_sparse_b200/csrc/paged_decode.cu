@@ -56,7 +56,7 @@ static_assert(1 << kTileLog2 == kTileKeys, "tile");
 // sequences of 1048576 keys take 945 us, their near tiles being larger, and 64 of
 // up to 8192 86 us, some CTAs holding ten of them; with them 893 and 83.
 constexpr int kTileCost = 16, kPieceCost = 64;
-constexpr int kPerLane = 4;  // sequences that a lane sums in a small batch
+constexpr int kPerLane = 8;  // sequences that a lane sums in a small batch
 constexpr int kMaxTilePages = 4;  // boxes of 16 keys
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;

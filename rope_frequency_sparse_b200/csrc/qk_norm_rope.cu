@@ -139,6 +139,20 @@ struct Turn {
   uint64_t ac[4], bs[4], as[4], bc[4];
 };
 
+// Cosine and sine of pair 8 c + k at position p of its axis.
+template <int D, bool kFast>
+__device__ __forceinline__ void pair_angle(const RotaryShared* sh, int c, int k, int p, float* sn, float* cs) {
+  const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(p)) * sh->turns[k * (D / 16) + c];
+  const float part = static_cast<float>(static_cast<int>(t >> 32));  // of 2^32 of a turn, in [-1/2, 1/2)
+  if (kFast) {
+    const float x = 1.4629180792671596e-9f * part;  // 2 pi / 2^32
+    *sn = __sinf(x);
+    *cs = __cosf(x);
+  } else {
+    sincospif(4.656612873077393e-10f * part, sn, cs);  // 2 / 2^32
+  }
+}
+
 template <int D, bool kFast>
 __device__ __forceinline__ void chunk_turn(Turn& turn, const RotaryShared* sh, int c, const Position& pos, int n_axes, bool norm,
                                            const float* wa, const float* wb) {
@@ -151,16 +165,8 @@ __device__ __forceinline__ void chunk_turn(Turn& turn, const RotaryShared* sh, i
   for (int k = 0; k < 8; ++k) {
     int p = common;
     if (chunk < 0) p = on_axis(sh->axis[k * NC + c]);
-    const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(p)) * sh->turns[k * NC + c];
-    const float part = static_cast<float>(static_cast<int>(t >> 32));  // of 2^32 of a turn, in [-1/2, 1/2)
     float sn, cs;
-    if (kFast) {
-      const float x = 1.4629180792671596e-9f * part;  // 2 pi / 2^32
-      sn = __sinf(x);
-      cs = __cosf(x);
-    } else {
-      sincospif(4.656612873077393e-10f * part, &sn, &cs);  // 2 / 2^32
-    }
+    pair_angle<D, kFast>(sh, c, k, p, &sn, &cs);
     m[0][k] = norm ? wa[k] * cs : cs;
     m[1][k] = norm ? -wb[k] * sn : -sn;
     m[2][k] = norm ? wa[k] * sn : sn;
@@ -200,6 +206,38 @@ __device__ __forceinline__ void apply(const Turn& t, const uint64_t* a, const ui
   for (int k = 0; k < 4; ++k) {
     unpack2(fmul2(r, ffma2(a[k], t.ac[k], fmul2(b[k], t.bs[k]))), ya[2 * k], ya[2 * k + 1]);
     unpack2(fmul2(r, ffma2(a[k], t.as[k], fmul2(b[k], t.bc[k]))), yb[2 * k], yb[2 * k + 1]);
+  }
+}
+
+// One bf16 head's chunk normed, turned and rounded, two pairs at a time: for a thread
+// with a single head, which needs no map kept.  Every lane of the warp calls it; the
+// sum of squares is taken whether the lane's row has a norm or not.
+template <int D, bool kHalf>
+__device__ __forceinline__ void turn_one(uint32_t* y, const Chunk<__nv_bfloat16, kHalf>& in,
+                                         const Chunk<__nv_bfloat16, kHalf>& weight, bool norm, float eps,
+                                         const RotaryShared* sh, int c, const Position& pos, int n_axes) {
+  constexpr int NC = D / 16;
+  float a[8], b[8];
+  in.pairs(a, b);
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) ss += a[k] * a[k] + b[k] * b[k];
+#pragma unroll
+  for (int off = 1; off < NC; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  const float scale = norm ? rsqrtf(ss * (1.0f / D) + eps) : 1.f;
+  const int chunk = n_axes > 1 ? sh->chunk_axis[c] : 0;
+  auto on_axis = [&](int a) { return a == 1 ? pos.at[1] : a == 2 ? pos.at[2] : a == 3 ? pos.at[3] : pos.at[0]; };
+  const int common = on_axis(chunk);
+  float wa[8], wb[8];
+  if (norm) weight.pairs(wa, wb);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    int p = common;
+    if (chunk < 0) p = on_axis(sh->axis[k * NC + c]);
+    float sn, cs;
+    pair_angle<D, true>(sh, c, k, p, &sn, &cs);
+    const float u = norm ? a[k] * wa[k] * scale : a[k], v = norm ? b[k] * wb[k] * scale : b[k];
+    y[k] = pack_bf16x2(u * cs - v * sn, u * sn + v * cs);
   }
 }
 
@@ -271,8 +309,9 @@ template <typename T, int D, bool kHalf>
 static cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s) {
   const long long chunks = static_cast<long long>(p.tokens) * (D / 16);
   const unsigned blocks = static_cast<unsigned>((chunks + kNrThreads - 1) / kNrThreads);
-  // kRows heads a thread once that still leaves every SM 512 threads
-  const bool many = chunks * (p.hq + p.hkv) >= 148LL * 512 * kRows;
+  // kRows heads a thread once that still leaves every SM 128 threads (1024 tokens of 28 + 4
+  // heads of 128: 4.6 us, one head a thread 6.6; 64 tokens 2.5 and 2.0)
+  const bool many = chunks * (p.hq + p.hkv) >= 148LL * 128 * kRows;
   if (!many) return launch_pdl(qk_norm_rope_kernel<T, D, 1, kHalf>, dim3(blocks, p.hq + p.hkv), kNrThreads, 0, s, p);
   const int groups = (p.hq + kRows - 1) / kRows + (p.hkv + kRows - 1) / kRows;
   return launch_pdl(qk_norm_rope_kernel<T, D, kRows, kHalf>, dim3(blocks, groups), kNrThreads, 0, s, p);
@@ -380,19 +419,8 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
 #pragma unroll
     for (int which = 0; which < 2; ++which)
       load32(old[which], reinterpret_cast<const bf16*>(bounds_row<D>(p, page, r, which, c)));
-  float x[8], z[8], wa[8], wb[8];
-  uint64_t x2[4], z2[4];
-  Turn turn;
-  if (w) cw.pairs(wa, wb);
-  chunk_turn<D, true>(turn, &sh, c, pos, p.pos ? p.rot.n_axes : 1, w != nullptr, wa, wb);
-  in.pairs(x, z);
-  pack_pairs(x, x2);
-  pack_pairs(z, z2);
-  const float scale = norm_scale<D>(x2, z2, p.eps);  // a warp's rows may have a norm and none
-  apply(turn, x2, z2, w ? scale : 1.f, x, z);
   uint32_t y[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[k], z[k]);
+  turn_one<D, kHalf>(y, in, cw, w != nullptr, p.eps, &sh, c, pos, p.pos ? p.rot.n_axes : 1);
   if (!live) return;
   if (!key) return store32(static_cast<bf16*>(p.q_out) + (static_cast<long long>(b) * hq + r - p.hkv) * D + 16 * c, y, p.wide);
   if (page < 0) return;
@@ -547,18 +575,9 @@ __global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = v_next[k];
     if (t0 + kTok < n) fetch(t + kTok);
-    float x[8], z[8], wa[8], wb[8];
-    uint64_t x2[4], z2[4];
-    Turn turn;
-    if (w) cw.pairs(wa, wb);
-    chunk_turn<D, true>(turn, &sh, c, pos, axes, w != nullptr, wa, wb);
-    in.pairs(x, z);
-    pack_pairs(x, x2);
-    pack_pairs(z, z2);
-    apply(turn, x2, z2, w ? norm_scale<D>(x2, z2, p.eps) : 1.f, x, z);
+    turn_one<D, kHalf>(y, in, cw, w != nullptr, p.eps, &sh, c, pos, axes);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      y[k] = pack_bf16x2(x[k], z[k]);
       lo[k] = min_bf16x2(lo[k], y[k]);
       hi[k] = max_bf16x2(hi[k], y[k]);
     }
