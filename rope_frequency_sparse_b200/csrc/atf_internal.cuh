@@ -119,6 +119,7 @@ struct PagedDecodeParams {
   float2* sums;           // [kPagedCtas][2][8] their maxima and row sums
   int4* meta;             // [kPagedCtas]: split sequence, kv head, last CTA of the sequences begun by each CTA
   int batch, hq, hkv, d, page_log2, max_pages, num_pages, n_sel;
+  int tile_keys;          // keys of the TMA boxes and tiles: 64, or 128 with d = 64
   unsigned int* err;
   Windows win;
 };
@@ -137,7 +138,10 @@ struct PageSelectParams {
 
 // CTAs of a paged decode: one per SM of a B200.
 constexpr int kPagedCtas = 148;
-constexpr int kPagedTileKeys = 64;  // keys of a tile of its work
+// Keys of a tile of its work, of up to `keys` keys of all sequences and kv heads: 64, but
+// 128 where heads of 64 fill every CTA with eight tiles of 64 or more.  450091 keys of 4
+// kv heads of 64 take 76 us in tiles of 64, 52 in tiles of 128; 777 keys 6.9 and 7.9.
+constexpr int paged_tile_keys(int d, long long keys) { return d == 64 && keys >= 8LL * 64 * kPagedCtas ? 128 : 64; }
 
 // Codes of the device error word for bad data in device arrays (the entry is
 // skipped); bounded waits that expired record smaller codes.

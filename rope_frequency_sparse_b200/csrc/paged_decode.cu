@@ -48,44 +48,45 @@ constexpr int kPdConsumers = 4 * kPdGroups;
 constexpr int kPdProducers = 4;  // warps that fill the ring, every fourth tile each
 constexpr int kPdJoiners = 4;    // warps that join the consumers' states at the end of a piece
 constexpr int kPdThreads = (kPdConsumers + kPdProducers + kPdJoiners) * 32;
-constexpr int kTileKeys = kPagedTileKeys;
-constexpr int kTileLog2 = 6;
-static_assert(1 << kTileLog2 == kTileKeys, "tile");
-// What a tile and a sequence's head cost beside their bytes, in 32-byte reads a key.
-// Measured in two batches (28 query and 4 kv heads of 128): without them four
-// sequences of 1048576 keys take 945 us, their near tiles being larger, and 64 of
-// up to 8192 86 us, some CTAs holding ten of them; with them 893 and 83.
-constexpr int kTileCost = 16, kPieceCost = 64;
-constexpr int kPerLane = 8;  // sequences that a lane sums in a small batch
-constexpr int kMaxTilePages = 4;  // boxes of 16 keys
+constexpr int kPerLane = 4;  // sequences that a lane sums in a small batch
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D>
+template <int D, int KB_>
 struct PdCfg {
   static constexpr int NC = D / 16;
-  static constexpr int HALF = kTileKeys * D * 2;  // bytes of a tile's keys, and of its values
+  static constexpr int KB = KB_;                   // blocks of 16 keys of a tile that a warp takes
+  static constexpr int TILE = 64 * KB;             // keys of a tile of the work
+  static constexpr int TILE_LOG2 = KB == 2 ? 7 : 6;
+  static constexpr int BOXES = TILE / 16;          // of the smallest pages
+  static constexpr int HALF = TILE * D * 2;        // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int NSTG = D == 128 ? 5 : 8;
+  static constexpr int NSTG = D == 128 ? 5 : KB == 2 ? 6 : 8;
+  // What a tile and a sequence's head cost beside their bytes, in 32-byte reads a key.
+  // Measured in two batches (28 query and 4 kv heads of 128): without them four
+  // sequences of 1048576 keys take 945 us, their near tiles being larger, and 64 of
+  // up to 8192 86 us, some CTAs holding ten of them; with them 893 and 83.
+  static constexpr int TILE_COST = 16 / KB, PIECE_COST = 64 / KB;
   static constexpr int Q = 8 * D * 2;
   static constexpr int OROW = D + 4;              // padded so that a warp's stores spread over the banks
   static constexpr int MERGE = kPdConsumers * 8 * OROW * 4;
 };
 
+template <int D, int KB>
 struct __align__(16) StageInfo {
   int4 tile;                // keys of the sequence; first chunk loaded | flags | slot + 1; sequence; kv head
-  int2 box[kMaxTilePages];  // first key of each box of the tile, and its live keys (0: no such page)
+  int2 box[PdCfg<D, KB>::BOXES];  // first key of each box of the tile, and its live keys (0: no such page)
 };
 // In tile.y: bits 0-7 the first chunk loaded, 8-10 these flags, 16-17 one more than the
 // CTA's partial slot (0: the whole sequence, write the output).
 constexpr int kFirst = 0x100, kLast = 0x200, kEnd = 0x400;
 
-template <int D>
+template <int D, int KB>
 struct PdShared {
-  uint64_t full[PdCfg<D>::NSTG], empty[PdCfg<D>::NSTG];
+  uint64_t full[PdCfg<D, KB>::NSTG], empty[PdCfg<D, KB>::NSTG];
   uint64_t left, joined;  // the consumers have left their states; the joiners are done with them
-  StageInfo info[PdCfg<D>::NSTG];
+  StageInfo<D, KB> info[PdCfg<D, KB>::NSTG];
   int w[kMaxPairs];
   int abort;
   long long scan[kPdThreads / 32];
@@ -96,9 +97,9 @@ struct PdShared {
   int passed;                                      // stages that the first consumer has passed
 };
 
-template <int D>
+template <int D, int KB>
 constexpr int pd_smem_bytes() {
-  return PdCfg<D>::NSTG * (PdCfg<D>::STAGE + PdCfg<D>::Q) + PdCfg<D>::MERGE + static_cast<int>(sizeof(PdShared<D>)) + 1024;
+  return PdCfg<D, KB>::NSTG * (PdCfg<D, KB>::STAGE + PdCfg<D, KB>::Q) + PdCfg<D, KB>::MERGE + static_cast<int>(sizeof(PdShared<D, KB>)) + 1024;
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -118,36 +119,40 @@ __device__ __forceinline__ int clamped_len(const PagedDecodeParams& p, int b) {
 }
 
 // Tiles of a sequence (at least one, so that an empty sequence writes its zeros).
+template <int TILE>
 __device__ __forceinline__ int tiles_of(const PagedDecodeParams& p, int len) {
   int keys = len;
   if (p.selected) {
     const int pages = (len + (1 << p.page_log2) - 1) >> p.page_log2;
     keys = min(p.n_sel, pages) << p.page_log2;
   }
-  return max(1, (keys + kTileKeys - 1) / kTileKeys);
+  return max(1, (keys - 1) / TILE + 1);
 }
 
 // Weight of tiles [0, t) of a sequence in 32-byte reads a key: value row plus
-// live key chunks, and the costs above.  Chunk c is out of reach of the whole tiles before (len - W -
-// 1) / 64, W the window of its last pair.  A list of pages weighs full rows.
-template <int NC>
+// live key chunks, and the costs above.  Chunk c is out of reach of the whole tiles
+// before (len - W - 1) / TILE, W the window of its last pair.  A list of pages weighs
+// full rows.
+template <int D, int KB>
 struct TileWeight {
+  using C = PdCfg<D, KB>;
+  static constexpr int NC = C::NC;
   int dead[NC];
   __device__ __forceinline__ TileWeight(const PagedDecodeParams& p, const int* w, int len) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, len - w[8 * c + 7] - 1) >> kTileLog2;
+    for (int c = 0; c < NC; ++c) dead[c] = p.selected ? 0 : max(0, len - w[8 * c + 7] - 1) >> C::TILE_LOG2;
   }
   __device__ __forceinline__ int operator()(int t) const {
-    int x = (2 * NC + kTileCost) * t;
+    int x = (2 * NC + C::TILE_COST) * t;
 #pragma unroll
     for (int c = 0; c < NC; ++c) x -= min(t, dead[c]);
-    return t > 0 ? x + kPieceCost : 0;
+    return t > 0 ? x + C::PIECE_COST : 0;
   }
 };
 
 // Smallest t in [0, tiles] with weight(t) >= x, by a warp: 32 points at a time.
-template <int NC>
-__device__ __forceinline__ int tile_at(const TileWeight<NC>& weight, int tiles, int x) {
+template <int D, int KB>
+__device__ __forceinline__ int tile_at(const TileWeight<D, KB>& weight, int tiles, int x) {
   int lo = 0, hi = tiles;
   while (lo < hi) {
     const int step = (hi - lo + 32) >> 5;  // hi is a candidate too
@@ -174,59 +179,75 @@ struct RingPos {
   }
 };
 
-// S^T of a warp's 16 keys over the chunks CLO..NC-1, the first `dirty` chunks
+// A block of 16 keys that a warp takes of a tile.
+struct Block {
+  uint32_t k_at;  // this lane's first row of its keys
+  int far;        // distance of its first key
+  int dirty;      // chunks of which some pair is out of reach of some key: the first ones
+};
+
+// S^T of a warp's KB blocks over the chunks CLO..NC-1, the first `dirty` chunks
 // masked by their pairs' windows.  Every load is issued before the first product.
-template <int NC, int CLO>
-__device__ __forceinline__ void qk_tile(float* s, uint32_t at, uint32_t cbytes, uint32_t odd, const uint32_t (*qf)[2], int dirty,
-                                        int far, const int* w, int krow, int kcol) {
-  uint32_t a[NC - CLO][4];
+template <int NC, int CLO, int KB>
+__device__ __forceinline__ void qk_tile(float (*s)[4], const Block* blocks, uint32_t cbytes, uint32_t odd, const uint32_t (*qf)[2],
+                                        const int* w, int krow, int kcol) {
+  uint32_t a[KB][NC - CLO][4];
 #pragma unroll
-  for (int j = 0; j < NC - CLO; ++j) ldsm_x4((at + j * cbytes) ^ ((j & 1) ? odd : 0u), a[j]);
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int j = 0; j < NC - CLO; ++j) ldsm_x4((blocks[kb].k_at + j * cbytes) ^ ((j & 1) ? odd : 0u), a[kb][j]);
+  float t[KB][4];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) t[kb][0] = t[kb][1] = t[kb][2] = t[kb][3] = 0.f;
 #pragma unroll
   for (int j = 0; j < NC - CLO; ++j) {
     constexpr int c0 = CLO;
     const int c = c0 + j;
-    if (c < dirty) {  // some pair of the chunk is out of reach of some key
-      const int wl = w[8 * c + kcol], wh = w[8 * c + 4 + kcol];
-      if (far - krow > wl) a[j][0] = 0u;
-      if (far - krow - 8 > wl) a[j][1] = 0u;
-      if (far - krow > wh) a[j][2] = 0u;
-      if (far - krow - 8 > wh) a[j][3] = 0u;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      if (c < blocks[kb].dirty) {  // some pair of the chunk is out of reach of some key
+        const int far = blocks[kb].far, wl = w[8 * c + kcol], wh = w[8 * c + 4 + kcol];
+        if (far - krow > wl) a[kb][j][0] = 0u;
+        if (far - krow - 8 > wl) a[kb][j][1] = 0u;
+        if (far - krow > wh) a[kb][j][2] = 0u;
+        if (far - krow - 8 > wh) a[kb][j][3] = 0u;
+      }
+      mma_bf16_16816((j & 1) ? t[kb] : s[kb], a[kb][j], qf[c][0], qf[c][1]);
     }
-    mma_bf16_16816((j & 1) ? t : s, a[j], qf[c][0], qf[c][1]);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) s[e] += t[e];
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[kb][e] += t[kb][e];
 }
 
-template <int NC, int CLO>
-__device__ __forceinline__ void qk_from(int clo, float* s, uint32_t at, uint32_t cbytes, uint32_t odd,
-                                        const uint32_t (*qf)[2], int dirty, int far, const int* w, int krow, int kcol) {
+template <int NC, int CLO, int KB>
+__device__ __forceinline__ void qk_from(int clo, float (*s)[4], const Block* blocks, uint32_t cbytes, uint32_t odd,
+                                        const uint32_t (*qf)[2], const int* w, int krow, int kcol) {
   if constexpr (CLO < NC - 1) {
-    if (clo != CLO) return qk_from<NC, CLO + 1>(clo, s, at, cbytes, odd, qf, dirty, far, w, krow, kcol);
+    if (clo != CLO) return qk_from<NC, CLO + 1, KB>(clo, s, blocks, cbytes, odd, qf, w, krow, kcol);
   }
-  qk_tile<NC, CLO>(s, at, cbytes, odd, qf, dirty, far, w, krow, kcol);
+  qk_tile<NC, CLO, KB>(s, blocks, cbytes, odd, qf, w, krow, kcol);
 }
 
 }  // namespace
 
-template <int D>
+template <int D, int KB>
 __global__ void __launch_bounds__(kPdThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedDecodeParams p) {
-  using C = PdCfg<D>;
+  using C = PdCfg<D, KB>;
   constexpr int NC = C::NC, NSTG = C::NSTG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sStage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sStage + NSTG * C::STAGE;
   float* sO = reinterpret_cast<float*>(sQ + NSTG * C::Q);
-  PdShared<D>* sh = reinterpret_cast<PdShared<D>*>(reinterpret_cast<uint8_t*>(sO) + C::MERGE);
+  PdShared<D, KB>* sh = reinterpret_cast<PdShared<D, KB>*>(reinterpret_cast<uint8_t*>(sO) + C::MERGE);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
   const int G = p.hq / p.hkv;
-  const int box_log2 = min(p.page_log2, kTileLog2), box = 1 << box_log2;  // keys of a TMA box
+  const int box_log2 = min(p.page_log2, C::TILE_LOG2), box = 1 << box_log2;  // keys of a TMA box
 
   if (tid == 0) {
     for (int s = 0; s < NSTG; ++s) {
@@ -252,7 +273,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   const bool alone = p.batch <= 32 * kPerLane;
   long long total = 0, base = 0;  // weight of all, and before the piece's first sequence
   int b = -1, len = 0;            // the piece's first sequence (-1: no piece)
-  auto weight_of = [&](int n) { return static_cast<long long>(TileWeight<NC>(p, sh->w, n)(tiles_of(p, n))) * p.hkv; };
+  auto weight_of = [&](int n) { return static_cast<long long>(TileWeight<D, KB>(p, sh->w, n)(tiles_of<C::TILE>(p, n))) * p.hkv; };
   auto scan = [&](long long x, int lanes) {  // inclusive, over the warp's first lanes
     for (int off = 1; off < lanes; off <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, x, off);
@@ -324,17 +345,17 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     const int pw = warp - kPdConsumers;
     int it = 0;  // stages passed
     bool ok = true, has_partial0 = false, has_meta = false;
-    const int ps = 1 << p.page_log2, sub_log2 = p.page_log2 - box_log2, boxes = kTileKeys >> box_log2;
+    const int ps = 1 << p.page_log2, sub_log2 = p.page_log2 - box_log2, boxes = C::TILE >> box_log2;
     const uint32_t box_bytes = static_cast<uint32_t>(D * 2) << box_log2;
     const long long from = piece_begin(total, cta), to = piece_begin(total, cta + 1);
     int hk = 0;
     bool more = b >= 0;
     while (more && ok) {
-      const int tiles = tiles_of(p, len);
-      const TileWeight<NC> weight(p, sh->w, len);
+      const int tiles = tiles_of<C::TILE>(p, len);
+      const TileWeight<D, KB> weight(p, sh->w, len);
       const int unit = weight(tiles);
       while (from >= base + unit) base += unit, ++hk;  // heads before the piece, at its beginning only
-      const int t0 = from > base ? tile_at<NC>(weight, tiles, static_cast<int>(from - base)) : 0;
+      const int t0 = from > base ? tile_at<D, KB>(weight, tiles, static_cast<int>(from - base)) : 0;
       const int pages = (len + ps - 1) >> p.page_log2;
       const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
       const int count = list ? min(p.n_sel, pages) : pages;
@@ -356,11 +377,11 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       int logical_next = listed(t0 * boxes + lane);
       int page_next = in_pool(logical_next);
       int logical_far = listed(t0 * boxes + 32 + lane);
-      const int t1 = to >= base + unit ? tiles : tile_at<NC>(weight, tiles, static_cast<int>(to - base));
+      const int t1 = to >= base + unit ? tiles : tile_at<D, KB>(weight, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
         const int slot = t0 > 0 ? 0 : t1 < tiles ? 1 : -1;
         if (slot == 0) has_partial0 = true;
-        for (int tg = t0; tg < t1 && ok; tg += 32 >> (kTileLog2 - box_log2)) {
+        for (int tg = t0; tg < t1 && ok; tg += 32 >> (C::TILE_LOG2 - box_log2)) {
           // this lane's box of the group
           const int i = tg * boxes + lane;
           int logical = logical_next, page = page_next;
@@ -386,16 +407,16 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
             for (int c = 0; c < NC - 1; ++c) clo += sh->w[8 * c + 7] < len - 1 - near;
           }
-          const int tile = i >> (kTileLog2 - box_log2);  // the tile of this lane's box
+          const int tile = i >> (C::TILE_LOG2 - box_log2);  // the tile of this lane's box
           const bool lead = (lane & (boxes - 1)) == 0;
-          const int tg1 = min(t1, tg + (32 >> (kTileLog2 - box_log2)));
+          const int tg1 = min(t1, tg + (32 >> (C::TILE_LOG2 - box_log2)));
           for (int t = tg; t < tg1; ++t, ++it, ring.next()) {
             if (it % kPdProducers != pw) continue;
             if (it >= NSTG && !warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x501)) {
               ok = false;
               break;
             }
-            StageInfo* info = &sh->info[ring.st];
+            StageInfo<D, KB>* info = &sh->info[ring.st];
             if (tile == t) {
               info->box[lane & (boxes - 1)] = make_int2(key0, keys);
               if (lead) {
@@ -492,8 +513,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kPdConsumers; ++w) {
+          if (sh->mw[w][g] == -INFINITY) continue;  // no key of the piece
           const float4 x = *reinterpret_cast<const float4*>(&sO[(w * 8 + g) * C::OROW + e]);
-          const float f = top == -INFINITY ? 0.f : ex2_approx(sh->mw[w][g] - top);
+          const float f = ex2_approx(sh->mw[w][g] - top);
           acc.x += x.x * f, acc.y += x.y * f, acc.z += x.z * f, acc.w += x.w * f;
           sum += sh->lw[w][g] * f;
         }
@@ -518,17 +540,24 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   const float scale = kLog2e * rsqrtf(static_cast<float>(D));
   const int kcol = lane & 3, krow = lane >> 2;  // this lane's pair in a half chunk / head pair, and key row / dim row
   const int group = warp >> 2;
-  // this warp's 16 keys of a tile: box and slot in it
-  const int bx = (16 * (warp & 3)) >> box_log2, off = (16 * (warp & 3)) & (box - 1);
+  // this warp's blocks of a tile: box, slot in it, and this lane's rows
   const uint32_t cbytes = 32u << box_log2, vhalf = 128u << box_log2;
-  const int krow_ld = off + (lane & 15), vrow_ld = off + (lane & 7) + ((lane >> 4) << 3);
-  // a chunk's rows of four keys, 128 bytes each, lie 16-byte units swizzled by the
-  // row's number in its 1024 bytes; chunks of 16 keys are half as long, so every
-  // other one starts at row 4
-  const uint32_t k_at = bx * (static_cast<uint32_t>(D * 2) << box_log2) + (krow_ld >> 2) * 128 +
-                        ((((krow_ld & 3) * 2 + (lane >> 4)) ^ ((krow_ld >> 2) & 7)) << 4);
   const uint32_t k_odd = box == 16 ? 64u : 0u;
-  const uint32_t v_at = C::HALF + bx * (static_cast<uint32_t>(D * 2) << box_log2) + vrow_ld * 128;
+  int bx[KB], off[KB];
+  uint32_t k_at[KB], v_at[KB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int key = 16 * ((warp & 3) * KB + kb);
+    bx[kb] = key >> box_log2, off[kb] = key & (box - 1);
+    const uint32_t at = bx[kb] * (static_cast<uint32_t>(D * 2) << box_log2);
+    // a chunk's rows of four keys, 128 bytes each, lie 16-byte units swizzled by the
+    // row's number in its 1024 bytes; chunks of 16 keys are half as long, so every
+    // other one starts at row 4
+    const int krow_ld = off[kb] + (lane & 15), vrow_ld = off[kb] + (lane & 7) + ((lane >> 4) << 3);
+    k_at[kb] = at + (krow_ld >> 2) * 128 + ((((krow_ld & 3) * 2 + (lane >> 4)) ^ ((krow_ld >> 2) & 7)) << 4);
+    v_at[kb] = C::HALF + at + vrow_ld * 128;
+  }
+  const int vrow_unit = lane & 7;  // of every block's row, modulo 8
   uint32_t qf[NC][2];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2*kcol, 2*kcol + 1
   float o[D / 16][4];  // O^T: dims 16u + krow (+8), heads 2*kcol (+1)
@@ -548,7 +577,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x503)) return;
     ring.next();
     const int4 tile = sh->info[st].tile;
-    const int2 my = sh->info[st].box[bx];
+    int2 my[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) my[kb] = sh->info[st].box[bx[kb]];
     const int flags = tile.y;
     if (tid == 0) *static_cast<volatile int*>(&sh->passed) = ++passed;
     if (flags & kEnd) {
@@ -567,34 +598,50 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     }
     if (turn == group) {
-      const int live = my.y - off;                  // live keys from this warp's first on
-      const int far = tile.x - 1 - (my.x + off);  // distance of its first key
       const uint32_t stg = smem_u32(sStage + st * C::STAGE);
-
-      // ---- S^T of 16 keys, pairs beyond their window zeroed
-      const int dirty = __popc(__ballot_sync(0xffffffffu, far > w_first));
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      qk_from<NC, 0>(flags & 0xff, s, stg + k_at, cbytes, k_odd, qf, dirty, far, sh->w, krow, kcol);
-      // the values' first half is fetched while the softmax runs
-      uint32_t va[D / 32][4];
-      auto load_v = [&](int u0) {
+      int live[KB];  // live keys from the block's first on
+      Block blocks[KB];
+      float s[KB][4];
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
+      for (int kb = 0; kb < KB; ++kb) {
+        live[kb] = my[kb].y - off[kb];
+        blocks[kb].k_at = stg + k_at[kb];
+        blocks[kb].far = tile.x - 1 - (my[kb].x + off[kb]);
+        blocks[kb].dirty = __popc(__ballot_sync(0xffffffffu, blocks[kb].far > w_first));
+        s[kb][0] = s[kb][1] = s[kb][2] = s[kb][3] = 0.f;
+      }
+
+      // ---- S^T, pairs beyond their window zeroed
+      qk_from<NC, 0, KB>(flags & 0xff, s, blocks, cbytes, k_odd, qf, sh->w, krow, kcol);
+      // the values go through registers in two halves, of the row or of the keys; the
+      // first is fetched while the softmax runs
+      constexpr int UPH = KB * D / 32;  // groups of 16 dims of a half
+      uint32_t va[UPH][4];
+      auto load_v = [&](int half) {
+        const int kb = KB == 1 ? 0 : half, u0 = KB == 1 ? half * UPH : 0;
+#pragma unroll
+        for (int u = 0; u < UPH; ++u) {
           const int dim = 16 * (u0 + u) + (lane & 8);
-          ldsm_x4_t(stg + v_at + ((u0 + u) >> 2) * vhalf + ((((dim & 63) >> 3) ^ (vrow_ld & 7)) << 4), va[u]);
+          ldsm_x4_t(stg + v_at[kb] + ((u0 + u) >> 2) * vhalf + ((((dim & 63) >> 3) ^ vrow_unit) << 4), va[u]);
         }
       };
       load_v(0);
       // ---- online softmax of heads 2*kcol, 2*kcol + 1.  The maximum that weights are
       // taken against is raised only where a logit is more than kSlack above it: they
       // stay below 2^kSlack, and most tiles need no reduction over the warp
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = krow + (e & 2) * 4 < live ? s[e] * scale : -INFINITY;
-      if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m[0] + kSlack || fmaxf(s[1], s[3]) > m[1] + kSlack)) {
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[kb][e] = krow + (e & 2) * 4 < live[kb] ? s[kb][e] * scale : -INFINITY;
+          top[e & 1] = fmaxf(top[e & 1], s[kb][e]);
+        }
+      if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
         float corr[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(s[e], s[e + 2]);
+          float mx = top[e];
 #pragma unroll
           for (int sh_ = 4; sh_ < 32; sh_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh_));
           mx = fmaxf(m[e], mx);
@@ -607,24 +654,29 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[u][e] *= corr[e & 1];
       }
-      float pr[4];
+      uint32_t pb[KB][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        pr[e] = ex2_approx(s[e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1]));  // no live key yet
-        l[e & 1] += pr[e];
+      for (int kb = 0; kb < KB; ++kb) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pr[e] = ex2_approx(s[kb][e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1]));  // no live key yet
+          l[e & 1] += pr[e];
+        }
+        pb[kb][0] = movmatrix_t(pack_bf16x2(pr[0], pr[1]));
+        pb[kb][1] = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
       }
-      const uint32_t pb0 = movmatrix_t(pack_bf16x2(pr[0], pr[1])), pb1 = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
       // ---- O^T += V^T P^T
-      // rows behind the last key may hold anything: their values count as zero
-      const int n = live - 2 * kcol;
-      const uint32_t keep0 = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u;
-      const uint32_t keep1 = n >= 10 ? 0xFFFFFFFFu : n == 9 ? 0xFFFFu : 0u;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (half) load_v(D / 32);
-        if (live < 16) {
+        const int kb = KB == 1 ? 0 : half, u0 = KB == 1 ? half * UPH : 0;
+        if (half) load_v(half);
+        if (live[kb] < 16) {  // rows behind the last key may hold anything: their values count as zero
+          const int n = live[kb] - 2 * kcol;
+          const uint32_t keep0 = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0xFFFFu : 0u;
+          const uint32_t keep1 = n >= 10 ? 0xFFFFFFFFu : n == 9 ? 0xFFFFu : 0u;
 #pragma unroll
-          for (int u = 0; u < D / 32; ++u) {
+          for (int u = 0; u < UPH; ++u) {
             va[u][0] &= keep0;
             va[u][1] &= keep0;
             va[u][2] &= keep1;
@@ -632,7 +684,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
           }
         }
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) mma_bf16_16816(o[half * (D / 32) + u], va[u], pb0, pb1);
+        for (int u = 0; u < UPH; ++u) mma_bf16_16816(o[u0 + u], va[u], pb[kb][0], pb[kb][1]);
       }
     }
     __syncwarp();
@@ -734,10 +786,10 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
   if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D>
+template <int D, int KB>
 static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  auto kern = paged_decode_kernel<D>;
-  constexpr int bytes = pd_smem_bytes<D>();
+  auto kern = paged_decode_kernel<D, KB>;
+  constexpr int bytes = pd_smem_bytes<D, KB>();
   static_assert(bytes <= 227 * 1024, "shared memory budget");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -754,7 +806,8 @@ static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, 
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  return p.d == 64 ? launch_pd<64>(p, tk, tv, s) : launch_pd<128>(p, tk, tv, s);
+  if (p.d == 128) return launch_pd<128, 1>(p, tk, tv, s);
+  return p.tile_keys == 128 ? launch_pd<64, 2>(p, tk, tv, s) : launch_pd<64, 1>(p, tk, tv, s);
 }
 
 }  // namespace atf

@@ -152,7 +152,7 @@ def test_bindings_refuse_wrong_tensors():
 
 # ------------------------------------------------------------------ the decode's division of its work
 
-CTAS, TILE, TILE_COST, PIECE_COST = 148, 64, 16, 64
+CTAS = 148
 
 
 def _cdiv0(a, b):  # C's division, towards zero
@@ -165,15 +165,16 @@ class Walk:
     def __init__(self, lens, hkv, d, theta, alpha, page, n_sel=None):
         self.w = [min(2 ** 31 - 1, int(x)) for x in oracle.windows(d, theta, alpha)[0]]
         self.nc, self.lens, self.hkv, self.page, self.n_sel = d // 16, lens, hkv, page, n_sel
+        self.tile = 64 if d == 128 or max(lens) * len(lens) * hkv < 8 * 64 * CTAS else 128
 
     def tiles(self, n):
         keys = n if self.n_sel is None else min(self.n_sel, -(-n // self.page)) * self.page
-        return max(1, -(-keys // TILE))
+        return max(1, -(-keys // self.tile))
 
     def weight(self, n, t):
-        x = (2 * self.nc + TILE_COST) * t + (PIECE_COST if t else 0)
+        x = 2 * self.nc * t + (16 * t + (64 if t else 0)) * 64 // self.tile
         if self.n_sel is None:
-            x -= sum(min(t, max(0, _cdiv0(n - self.w[8 * c + 7] - 1, TILE))) for c in range(self.nc))
+            x -= sum(min(t, max(0, _cdiv0(n - self.w[8 * c + 7] - 1, self.tile))) for c in range(self.nc))
         return x
 
     def at(self, n, x):
@@ -253,9 +254,9 @@ def test_tile_weights_count_the_live_chunks():
     for d, theta, alpha, n in [(128, 1e7, 1.0, 70000), (64, 1e4, 0.5, 9001), (128, 1.0001, 0.1, 400), (64, 1e4, 1.0, 1)]:
         walk = Walk([n], 1, d, theta, alpha, 64)
         for t in range(walk.tiles(n)):
-            near = n - 1 - (min(n, (t + 1) * TILE) - 1)
+            near = n - 1 - (min(n, (t + 1) * walk.tile) - 1)
             live = sum(1 for c in range(d // 16) if near <= walk.w[8 * c + 7])
-            assert walk.weight(n, t + 1) - walk.weight(n, t) == d // 16 + live + TILE_COST + (0 if t else PIECE_COST)
+            assert walk.weight(n, t + 1) - walk.weight(n, t) == d // 16 + live + (16 if t else 80) * 64 // walk.tile
 
 
 @pytest.mark.parametrize("seed", range(30))

@@ -296,6 +296,9 @@ def _check_decode(q, kp, vp, table, lens, theta, alpha, out, lse, selected=None)
     ([3000], 8, 1, 128, 16, 1.0001, 0.1),  # every window is 1: far keys have no pair in reach
     ([4000, 1, 1, 127, 128, 129] * 4, 7, 1, 128, 16, 1e7, math.inf), ([40000], 6, 3, 128, 64, 1e7, 0.5),
     ([0, 0, 0], 5, 1, 64, 16, 1e4, 1.0), ([1, 2, 3] * 90, 3, 3, 64, 32, 1e4, 1.0),
+    # enough keys for tiles of 128, whose pages end inside them
+    ([5000, 33, 129, 0] * 5, 6, 2, 64, 16, 1e4, 1.0), ([40000], 16, 2, 64, 128, 5e5, 0.5), ([100] * 400, 3, 3, 64, 64, 1e4, math.inf),
+    ([38000, 1], 4, 4, 64, 32, 1.0001, 0.1),
 ])
 def test_decode_against_oracle(lens, Hq, Hkv, d, page, theta, alpha):
     q, kp, vp, table, n = _decode_case(lens, Hq, Hkv, d, page, theta, alpha)
@@ -315,7 +318,8 @@ def test_decode_sharp_softmax_and_infinite_stale_slots():
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,d,page,n_sel", [
-    ([1000, 16, 0, 333], 28, 4, 128, 16, 9), ([5000, 200], 4, 2, 64, 64, 40), ([129], 8, 1, 128, 128, 1)])
+    ([1000, 16, 0, 333], 28, 4, 128, 16, 9), ([5000, 200], 4, 2, 64, 64, 40), ([129], 8, 1, 128, 128, 1),
+    ([2000, 100, 31, 0] * 10, 4, 2, 64, 32, 30)])
 def test_decode_over_listed_pages(lens, Hq, Hkv, d, page, n_sel):
     theta, alpha = 1e4, 1.0
     q, kp, vp, table, n = _decode_case(lens, Hq, Hkv, d, page, theta, alpha, seed=61)
