@@ -146,29 +146,40 @@ __device__ __forceinline__ void score_group(const PageSelectParams& p, int b, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) a4[i][0] = a4[i][1] = a4[i][2] = a4[i][3] = 0.f;
 #pragma unroll
-  for (int j = 0; j < 2 * NJ; ++j) {
-    uint32_t x[2][4], y[4];
+  for (int jp = 0; jp < NJ; ++jp) {
+    const int* w = sw + 16 * jp + 4 * kcol;
+    // out of reach of all 16 pages: nothing was read
+    if (!__any_sync(0xffffffffu, near[0] <= w[3] || near[1] <= w[3])) continue;
+    if (__any_sync(0xffffffffu, near[0] > w[0] || near[1] > w[0])) {  // out of reach in part
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 qj = qv[j % NJ];
-      const uint32_t w = k == 0 ? qj.x : k == 1 ? qj.y : k == 2 ? qj.z : qj.w;
-      const uint32_t negative = ((w >> 15) & 0x00010001u) * 0xFFFFu;
-      y[k] = j < NJ ? w & negative : w & ~negative;
-      const int window = sw[16 * (j % NJ) + 4 * kcol + k];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint4 z = v[r][j];
-        x[r][k] = k == 0 ? z.x : k == 1 ? z.y : k == 2 ? z.z : z.w;
-        if (near[r] > window) x[r][k] = 0u;
-      }
+        for (int j = jp; j < 2 * NJ; j += NJ) {
+          if (near[r] > w[0]) v[r][j].x = 0u;
+          if (near[r] > w[1]) v[r][j].y = 0u;
+          if (near[r] > w[2]) v[r][j].z = 0u;
+          if (near[r] > w[3]) v[r][j].w = 0u;
+        }
     }
+    const uint32_t q4[4] = {qv[jp].x, qv[jp].y, qv[jp].z, qv[jp].w};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t f[4] = {x[0][2 * h], x[1][2 * h], x[0][2 * h + 1], x[1][2 * h + 1]};
-      mma_bf16_16816(a4[(2 * j + h) & 3], f, y[2 * h], y[2 * h + 1]);
-      constexpr uint32_t kAbs = 0x7FFF7FFFu;
-      const uint32_t fa[4] = {f[0] & kAbs, f[1] & kAbs, f[2] & kAbs, f[3] & kAbs};
-      mma_bf16_16816(m, fa, y[2 * h] & kAbs, y[2 * h + 1] & kAbs);
+    for (int j = jp; j < 2 * NJ; j += NJ) {
+      const uint32_t x0[4] = {v[0][j].x, v[0][j].y, v[0][j].z, v[0][j].w};
+      const uint32_t x1[4] = {v[1][j].x, v[1][j].y, v[1][j].z, v[1][j].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t negative = ((q4[k] >> 15) & 0x00010001u) * 0xFFFFu;
+        y[k] = j < NJ ? q4[k] & negative : q4[k] & ~negative;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        const uint32_t f[4] = {x0[2 * h], x1[2 * h], x0[2 * h + 1], x1[2 * h + 1]};
+        const uint32_t fa[4] = {f[0] & kAbs, f[1] & kAbs, f[2] & kAbs, f[3] & kAbs};
+        mma_bf16_16816(a4[(2 * jp + h) & 3], f, y[2 * h], y[2 * h + 1]);
+        mma_bf16_16816(m, fa, y[2 * h] & kAbs, y[2 * h + 1] & kAbs);
+      }
     }
   }
   float a[4];
@@ -197,7 +208,7 @@ __device__ __forceinline__ void score_group(const PageSelectParams& p, int b, in
 }
 
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads, 5) page_score_kernel(const __grid_constant__ PageSelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 4) page_score_kernel(const __grid_constant__ PageSelectParams p) {
   const int hk = blockIdx.y % p.hkv, b = blockIdx.y / p.hkv;
   __shared__ int sw[kMaxPairs];
   for (int i = threadIdx.x; i < kMaxPairs; i += kScoreThreads) sw[i] = p.win.w[i];
