@@ -103,6 +103,7 @@ struct PagedAppendParams {
   const long long* pos;             // nullable: the slot
   int tokens, batch, hq, hkv, d, pairing, page_log2, max_pages, num_pages;
   long long items;                  // at least the pages that the new tokens of all sequences fall into
+  int threads;                      // of a CTA of a ragged append: 64, 128 or 256
   bool wide;                        // q_out and the pages are 32-byte aligned
   float eps;
   unsigned int* err;

@@ -223,6 +223,8 @@ atf_status atf_paged_append(const atf_paged_append_args* a, void* stream) {
   p.num_pages = static_cast<int>(a->num_pages);
   // a sequence with n > 0 new tokens touches at most (n - 1) / page + 2 pages
   p.items = (p.tokens >> p.page_log2) + 2LL * (p.batch < p.tokens ? p.batch : p.tokens);
+  const long long likely = ((p.tokens >> p.page_log2) + static_cast<long long>(p.batch)) * p.hkv;  // (page, kv head) items
+  p.threads = likely >= 600 ? 64 : likely >= 148 ? 128 : 256;
   p.wide = aligned32(p.q_out) && aligned32(p.k_pages) && aligned32(p.v_pages);
   if (p.cu && paged_append_blocks(p) > 0x7fffffffLL)
     return report_error(ATF_ERR_UNSUPPORTED, "%s: too many tokens, sequences and heads for one call", who);

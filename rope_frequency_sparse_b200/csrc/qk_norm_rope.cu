@@ -439,11 +439,15 @@ __global__ void __launch_bounds__(kNrThreads) paged_append_step_kernel(const __g
 
 // Ragged batch.  The first p.items * hkv CTAs own each the new tokens of one sequence
 // that fall into one page, for one kv head, so that the page's bounds have one
-// writer; the others kRows query heads each of kNrThreads / (d/16) rows.
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  constexpr int NC = D / 16, kTok = kNrThreads / NC;  // tokens in flight
-  constexpr int kWarps = kNrThreads / 32;
+// writer; the others kRows query heads each of kApThreads / (d/16) rows.
+// The CTA's size goes by the number of (page, kv head) items: of many, small CTAs leave
+// few threads without a token; of few, large ones take fewer passes over a page.  At
+// 64 / 128 / 256 threads: 2236 tokens of 60 sequences, 4 kv heads of 128, pages of 16:
+// 10.3 / 11.3 / 19 us; 1594 tokens of 16 sequences, 3 kv heads, pages of 128: 17.3 / 11.1 / 7.2.
+template <int D, bool kHalf, int kApThreads>
+__global__ void __launch_bounds__(kApThreads, kApThreads == 256 ? 2 : 640 / kApThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  constexpr int NC = D / 16, kTok = kApThreads / NC;  // tokens in flight
+  constexpr int kWarps = kApThreads / 32;
   __shared__ RotaryShared sh;
   __shared__ int s_item[3];  // sequence, first row, tokens
   __shared__ long long s_slot, s_scan[kWarps];  // first slot
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __gri
   const int kvh = static_cast<int>(blockIdx.x % p.hkv);
   if (tid == 0) s_item[2] = 0;
   long long before = 0;
-  for (int b0 = 0; b0 < p.batch && before <= item; b0 += kNrThreads) {
+  for (int b0 = 0; b0 < p.batch && before <= item; b0 += kApThreads) {
     const int b = b0 + tid;
     long long items = 0, r0 = 0, n = 0, s0 = -1;
     if (b < p.batch) {
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __gri
     }
   }
   __syncthreads();
-  for (int i = tid; i < D; i += kNrThreads) {  // word i % (D/2) of the minima, then of the maxima
+  for (int i = tid; i < D; i += kApThreads) {  // word i % (D/2) of the minima, then of the maxima
     const int which = i / (D / 2), x = i % (D / 2);
     uint32_t* dst = reinterpret_cast<uint32_t*>(bounds_row<D>(p, page, kvh, which, 0)) + x;
     uint32_t r = s_red[which][0][x];
@@ -610,14 +614,18 @@ __global__ void __launch_bounds__(kNrThreads, 5) paged_append_kernel(const __gri
 }
 
 long long paged_append_blocks(const PagedAppendParams& p) {
-  const int tok = kNrThreads / (p.d / 16), groups = p.q ? (p.hq + kRows - 1) / kRows : 0;
+  const int tok = p.threads / (p.d / 16), groups = p.q ? (p.hq + kRows - 1) / kRows : 0;
   return p.items * p.hkv + (p.tokens + tok - 1LL) / tok * groups;
 }
 
 template <int D, bool kHalf>
 static cudaError_t launch_append(const PagedAppendParams& p, cudaStream_t s) {
-  if (p.cu)
-    return launch_pdl(paged_append_kernel<D, kHalf>, static_cast<unsigned>(paged_append_blocks(p)), kNrThreads, 0, s, p);
+  if (p.cu) {
+    const unsigned blocks = static_cast<unsigned>(paged_append_blocks(p));
+    return p.threads == 64    ? launch_pdl(paged_append_kernel<D, kHalf, 64>, blocks, 64, 0, s, p)
+           : p.threads == 128 ? launch_pdl(paged_append_kernel<D, kHalf, 128>, blocks, 128, 0, s, p)
+                              : launch_pdl(paged_append_kernel<D, kHalf, 256>, blocks, 256, 0, s, p);
+  }
   const long long threads = static_cast<long long>(p.batch) * (p.hkv + (p.q ? p.hq : 0)) * (D / 16);
   return launch_pdl(paged_append_step_kernel<D, kHalf>, static_cast<unsigned>((threads + kNrThreads - 1) / kNrThreads), kNrThreads,
                     0, s, p);

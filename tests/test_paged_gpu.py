@@ -193,6 +193,8 @@ def _check_append(q, k, v, kp, vp, bounds, before, table, start, rows, pos, w, e
     ([31, 0, -1, 64], [1, 64, 9, 65], 6, 2, 64, 32, 0, 3, True, True),
     ([3], [1000], 8, 8, 128, 128, 1, 2, False, True),
     ([0] * 70, [1, 0, 2] * 23 + [5], 2, 1, 64, 64, 0, 1, True, False),
+    ([i % 40 - 1 for i in range(100)], [7 * i % 23 for i in range(100)], 8, 8, 64, 16, 1, 3, True, True),
+    ([9] * 40, [13, 70] * 20, 8, 4, 128, 32, 0, 1, True, True), ([100] * 160, [3] * 160, 4, 4, 128, 128, 1, 1, True, True),
 ])
 def test_append_against_oracle(start, new, Hq, Hkv, d, page, pairing, axes, norm, bounds):
     theta, eps, pad = 1e7, 1e-5, 3
