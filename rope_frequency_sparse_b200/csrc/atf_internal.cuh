@@ -142,7 +142,7 @@ constexpr int kPagedCtas = 148;
 // Keys of a tile of its work, of up to `keys` keys of all sequences and kv heads: 64, but
 // 128 where heads of 64 fill every CTA with eight tiles of 64 or more.  450091 keys of 4
 // kv heads of 64 take 76 us in tiles of 64, 52 in tiles of 128; 777 keys 6.9 and 7.9.
-constexpr int paged_tile_keys(int d, long long keys) { return d == 64 && keys >= 8LL * 64 * kPagedCtas ? 128 : 64; }
+constexpr int paged_tile_keys(int d, double keys) { return d == 64 && keys >= 8.0 * 64 * kPagedCtas ? 128 : 64; }
 
 // Codes of the device error word for bad data in device arrays (the entry is
 // skipped); bounded waits that expired record smaller codes.

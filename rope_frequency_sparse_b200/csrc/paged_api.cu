@@ -289,7 +289,7 @@ atf_status atf_paged_decode(const atf_paged_decode_args* a, void* stream) {
   const unsigned long long d = a->d, ps = a->page_size;
   const unsigned long long rows = static_cast<unsigned long long>(a->num_pages) * a->kv_heads;
   const unsigned long long kd[4] = {64, ps / 4, d / 16, rows}, ks[3] = {128, ps * 32, ps * d * 2};
-  const long long most = static_cast<long long>(a->selected && a->n_select < a->max_pages ? a->n_select : a->max_pages) * a->page_size;
+  const double most = static_cast<double>(a->selected && a->n_select < a->max_pages ? a->n_select : a->max_pages) * a->page_size;
   p.tile_keys = paged_tile_keys(a->d, most * a->batch * a->kv_heads);
   const unsigned box = a->page_size < p.tile_keys ? a->page_size : p.tile_keys;
   const unsigned int kb[4] = {64, box / 4, static_cast<unsigned>(d / 16), 1};

@@ -169,10 +169,14 @@ __device__ __forceinline__ int tile_at(const TileWeight<D, KB>& weight, int tile
   return lo;
 }
 
-// floor(total * j / kPagedCtas): where the piece of CTA j begins.
-__device__ __forceinline__ long long piece_begin(long long total, int j) {
-  return total / kPagedCtas * j + total % kPagedCtas * j / kPagedCtas;
-}
+// begin(j) = floor(total * j / kPagedCtas): where the piece of CTA j begins.
+struct Pieces {
+  long long each;
+  int rest;
+  __device__ __forceinline__ explicit Pieces(long long total)
+      : each(total / kPagedCtas), rest(static_cast<int>(total - each * kPagedCtas)) {}
+  __device__ __forceinline__ long long begin(int j) const { return each * j + rest * j / kPagedCtas; }
+};
 
 // A stage of the ring and the parity of its next phase.
 template <int N>
@@ -294,12 +298,16 @@ __global__ void __launch_bounds__(kPdThreads, 1)
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) n[j] = j < per && lane * per + j < p.batch ? clamped_len(p, lane * per + j) : -1;
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) mine += x[j] = n[j] >= 0 ? weight_of(n[j]) : 0;
+      for (int j = 0; j < kPerLane; ++j) {
+        x[j] = 0;
+        if (j < per) mine += x[j] = n[j] >= 0 ? weight_of(n[j]) : 0;  // a branch for the warp
+      }
       const long long incl = scan(mine, min(p.batch, 32));
       total = __shfl_sync(0xffffffffu, incl, min(p.batch, 32) - 1);
-      const long long from = piece_begin(total, cta);
+      const Pieces pieces(total);
+      const long long from = pieces.begin(cta);
       long long at = incl - mine;
-      const unsigned holds = __ballot_sync(0xffffffffu, from < piece_begin(total, cta + 1) && from >= at && from < incl);
+      const unsigned holds = __ballot_sync(0xffffffffu, from < pieces.begin(cta + 1) && from >= at && from < incl);
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) {
         if (b < 0 && n[j] >= 0 && from < at + x[j]) b = lane * per + j, len = n[j], base = at;
@@ -324,8 +332,9 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       if (i < warp) at += sh->scan[i];
       total += sh->scan[i];
     }
-    const long long from = piece_begin(total, cta);
-    if (from < piece_begin(total, cta + 1) && from >= at && from < at + mine) {
+    const Pieces pieces(total);
+    const long long from = pieces.begin(cta);
+    if (from < pieces.begin(cta + 1) && from >= at && from < at + mine) {
       for (int i = b0; i < b1; ++i) {
         const int n = clamped_len(p, i);
         const long long x = weight_of(n);
@@ -352,7 +361,8 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     bool ok = true, has_partial0 = false, has_meta = false;
     const int ps = 1 << p.page_log2, sub_log2 = p.page_log2 - box_log2, boxes = C::TILE >> box_log2;
     const uint32_t box_bytes = static_cast<uint32_t>(D * 2) << box_log2;
-    const long long from = piece_begin(total, cta), to = piece_begin(total, cta + 1);
+    const Pieces pieces(total);
+    const long long from = pieces.begin(cta), to = pieces.begin(cta + 1);
     int hk = 0;
     bool more = b >= 0;
     while (more && ok) {
@@ -451,11 +461,11 @@ __global__ void __launch_bounds__(kPdThreads, 1)
         if (slot == 1) {
           has_meta = true;
           const long long x = base + weight(tiles - 1);  // where its last tile begins
-          // the CTA whose piece holds x: the largest j with piece_begin(j) <= x
+          // the CTA whose piece holds x: the largest j with begin(j) <= x
           int lo = cta, hi = kPagedCtas - 1;
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (piece_begin(total, mid) <= x)
+            if (pieces.begin(mid) <= x)
               lo = mid;
             else
               hi = mid - 1;
