@@ -630,3 +630,48 @@ def test_scratch_and_outputs_of_a_call_on_a_given_stream():
     torch.cuda.synchronize()
     atf.atf_check()
     assert all(torch.equal(o, want) and torch.equal(s, sel) for o, s in got)
+
+
+def test_captured_behind_copies_and_events_of_other_streams():
+    """Graph nodes before the calls that are no kernels, and forks that join before and behind them."""
+    theta, alpha = 1e7, 1.0
+    q, kp, vp, table, n = _decode_case([5000, 700, 0], 28, 4, 128, 32, theta, alpha, seed=141)
+    bd = torch.stack([kp.amin(3).view(-1, 4, 128), kp.amax(3).view(-1, 4, 128)], 2).contiguous()
+    pos = torch.arange(3, device="cuda")[None].contiguous()
+    src = q.clone()
+
+    def calls(buf, side):
+        main = torch.cuda.current_stream()
+        buf["q"].copy_(src)
+        buf["n"].copy_(n)
+        atf.qk_norm_rope(buf["q"], buf["k"], theta, pos, q_out=buf["qn"], k_out=buf["kn"])
+        buf["qn"].zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            atf.page_select(buf["q"], bd, table, buf["n"], 32, 7, theta, alpha, selected=buf["sel"], workspace=buf["ws"][1])
+        atf.paged_decode(buf["q"], kp, vp, table, buf["n"], theta, alpha, out=buf["dense"], workspace=buf["ws"][0])
+        main.wait_stream(side)
+        atf.paged_decode(buf["q"], kp, vp, table, buf["n"], theta, alpha, selected=buf["sel"], out=buf["sparse"],
+                         workspace=buf["ws"][0])
+
+    def buffers():
+        need = max(atf.atf_paged_decode_workspace_bytes(3, 28, 4, 128), atf.atf_page_select_workspace_bytes(3, 4, table.shape[1]))
+        return dict(q=torch.empty_like(q), k=q[:, :4].contiguous(), n=torch.empty_like(n), qn=torch.empty_like(q),
+                    kn=torch.empty_like(q[:, :4].contiguous()), sel=torch.empty(3, 4, 7, dtype=torch.int32, device="cuda"),
+                    dense=torch.empty_like(q), sparse=torch.empty_like(q),
+                    ws=[torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)])
+
+    side = torch.cuda.Stream()
+    want, got = buffers(), buffers()
+    calls(want, side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(got, side)
+    for _ in range(4):
+        for x in ("dense", "sparse", "sel", "kn"):
+            got[x].fill_(1)
+        g.replay()
+    torch.cuda.synchronize()
+    atf.atf_check()
+    assert all(torch.equal(got[x], want[x]) for x in ("dense", "sparse", "sel", "kn"))
