@@ -723,7 +723,7 @@ static cudaError_t launch_select(const PageSelectParams& p, cudaStream_t s) {
   cudaError_t e = launch_pdl(page_score_kernel<D>, grid, kScoreThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   if (p.max_pages > kSelectThreads * kHeld) return launch_pdl(page_select_kernel<D, 0, false>, lists, kSelectThreads, 0, s, p);
-  return launch_pdl(page_select_kernel<D, kHeld, false>, lists, kSelectThreads, 0, s, p);
+  return launch_pdl(page_select_kernel<D, kHeld, false>, lists, p.max_pages <= 256 * kHeld ? 256 : kSelectThreads, 0, s, p);
 }
 
 cudaError_t launch_page_select(const PageSelectParams& p, cudaStream_t s) {

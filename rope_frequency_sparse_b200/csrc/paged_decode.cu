@@ -68,6 +68,9 @@ struct PdCfg {
   static constexpr int HALF = TILE * D * 2;        // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * HALF;
   static constexpr int NSTG = D == 128 ? 5 : KB == 2 ? 6 : 8;
+  // A producer last saw the tile NSTG + kPdProducers before its next one consumed; a parity
+  // wait needs the phase before the one it waits for completed, 2 NSTG tiles before.
+  static_assert(NSTG >= kPdProducers, "stages");
   // What a tile and a sequence's head cost beside their bytes, in 32-byte reads a key.
   // Measured in two batches (28 query and 4 kv heads of 128): without them four
   // sequences of 1048576 keys take 945 us, their near tiles being larger, and 64 of
