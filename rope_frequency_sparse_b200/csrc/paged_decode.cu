@@ -58,7 +58,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // log2 of the largest weight
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, int KB_>
+template <int D, int KB_, int NSTG_>
 struct PdCfg {
   static constexpr int NC = D / 16;
   static constexpr int KB = KB_;                   // blocks of 16 keys of a tile that a warp takes
@@ -67,7 +67,7 @@ struct PdCfg {
   static constexpr int BOXES = TILE / 16;          // of the smallest pages
   static constexpr int HALF = TILE * D * 2;        // bytes of a tile's keys, and of its values
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int NSTG = D == 128 ? 5 : KB == 2 ? 6 : 8;
+  static constexpr int NSTG = NSTG_;               // stages of the ring
   // A producer last saw the tile NSTG + kPdProducers before its next one consumed; a parity
   // wait needs the phase before the one it waits for completed, 2 NSTG tiles before.
   static_assert(NSTG >= kPdProducers, "stages");
@@ -81,20 +81,20 @@ struct PdCfg {
   static constexpr int MERGE = kPdConsumers * 8 * OROW * 4;
 };
 
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 struct __align__(16) StageInfo {
   int4 tile;                // keys of the sequence; first chunk loaded | flags | slot + 1; sequence; kv head
-  int2 box[PdCfg<D, KB>::BOXES];  // first key of each box of the tile, and its live keys (0: no such page)
+  int2 box[PdCfg<D, KB, NSTG>::BOXES];  // first key of each box of the tile, and its live keys (0: no such page)
 };
 // In tile.y: bits 0-7 the first chunk loaded, 8-10 these flags, 16-17 one more than the
 // CTA's partial slot (0: the whole sequence, write the output).
 constexpr int kFirst = 0x100, kLast = 0x200, kEnd = 0x400;
 
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 struct PdShared {
-  uint64_t full[PdCfg<D, KB>::NSTG], empty[PdCfg<D, KB>::NSTG];
+  uint64_t full[PdCfg<D, KB, NSTG>::NSTG], empty[PdCfg<D, KB, NSTG>::NSTG];
   uint64_t left, joined;  // the consumers have left their states; the joiners are done with them
-  StageInfo<D, KB> info[PdCfg<D, KB>::NSTG];
+  StageInfo<D, KB, NSTG> info[PdCfg<D, KB, NSTG>::NSTG];
   int w[kMaxPairs];
   int abort;
   long long scan[kPdThreads / 32];
@@ -105,9 +105,9 @@ struct PdShared {
   int passed;                                      // stages that the first consumer has passed
 };
 
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 constexpr int pd_smem_bytes() {
-  return PdCfg<D, KB>::NSTG * (PdCfg<D, KB>::STAGE + PdCfg<D, KB>::Q) + PdCfg<D, KB>::MERGE + static_cast<int>(sizeof(PdShared<D, KB>)) + 1024;
+  return PdCfg<D, KB, NSTG>::NSTG * (PdCfg<D, KB, NSTG>::STAGE + PdCfg<D, KB, NSTG>::Q) + PdCfg<D, KB, NSTG>::MERGE + static_cast<int>(sizeof(PdShared<D, KB, NSTG>)) + 1024;
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -141,9 +141,9 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeParams& p, int len) {
 // live key chunks, and the costs above.  Chunk c is out of reach of the whole tiles
 // before (len - W - 1) / TILE, W the window of its last pair.  A list of pages weighs
 // full rows.
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 struct TileWeight {
-  using C = PdCfg<D, KB>;
+  using C = PdCfg<D, KB, NSTG>;
   static constexpr int NC = C::NC;
   int dead[NC];
   __device__ __forceinline__ TileWeight(const PagedDecodeParams& p, const int* w, int len) {
@@ -159,8 +159,8 @@ struct TileWeight {
 };
 
 // Smallest t in [0, tiles] with weight(t) >= x, by a warp: 32 points at a time.
-template <int D, int KB>
-__device__ __forceinline__ int tile_at(const TileWeight<D, KB>& weight, int tiles, int x) {
+template <int D, int KB, int NSTG>
+__device__ __forceinline__ int tile_at(const TileWeight<D, KB, NSTG>& weight, int tiles, int x) {
   int lo = 0, hi = tiles;
   while (lo < hi) {
     const int step = (hi - lo + 32) >> 5;  // hi is a candidate too
@@ -244,17 +244,17 @@ __device__ __forceinline__ void qk_from(int clo, float (*s)[4], const Block* blo
 
 }  // namespace
 
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 __global__ void __launch_bounds__(kPdThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedDecodeParams p) {
-  using C = PdCfg<D, KB>;
-  constexpr int NC = C::NC, NSTG = C::NSTG;
+  using C = PdCfg<D, KB, NSTG>;
+  constexpr int NC = C::NC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sStage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sStage + NSTG * C::STAGE;
   float* sO = reinterpret_cast<float*>(sQ + NSTG * C::Q);
-  PdShared<D, KB>* sh = reinterpret_cast<PdShared<D, KB>*>(reinterpret_cast<uint8_t*>(sO) + C::MERGE);
+  PdShared<D, KB, NSTG>* sh = reinterpret_cast<PdShared<D, KB, NSTG>*>(reinterpret_cast<uint8_t*>(sO) + C::MERGE);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   const bool alone = p.batch <= 32 * kPerLane;
   long long total = 0, base = 0;  // weight of all, and before the piece's first sequence
   int b = -1, len = 0;            // the piece's first sequence (-1: no piece)
-  auto weight_of = [&](int n) { return static_cast<long long>(TileWeight<D, KB>(p, sh->w, n)(tiles_of<C::TILE>(p, n))) * p.hkv; };
+  auto weight_of = [&](int n) { return static_cast<long long>(TileWeight<D, KB, NSTG>(p, sh->w, n)(tiles_of<C::TILE>(p, n))) * p.hkv; };
   auto scan = [&](long long x, int lanes) {  // inclusive, over the warp's first lanes
     for (int off = 1; off < lanes; off <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, x, off);
@@ -370,10 +370,10 @@ __global__ void __launch_bounds__(kPdThreads, 1)
     bool more = b >= 0;
     while (more && ok) {
       const int tiles = tiles_of<C::TILE>(p, len);
-      const TileWeight<D, KB> weight(p, sh->w, len);
+      const TileWeight<D, KB, NSTG> weight(p, sh->w, len);
       const int unit = weight(tiles);
       while (from >= base + unit) base += unit, ++hk;  // heads before the piece, at its beginning only
-      const int t0 = from > base ? tile_at<D, KB>(weight, tiles, static_cast<int>(from - base)) : 0;
+      const int t0 = from > base ? tile_at<D, KB, NSTG>(weight, tiles, static_cast<int>(from - base)) : 0;
       const int pages = (len + ps - 1) >> p.page_log2;
       const int* list = p.selected ? p.selected + (static_cast<long long>(b) * p.hkv + hk) * p.n_sel : nullptr;
       const int count = list ? min(p.n_sel, pages) : pages;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       int logical_next = listed(t0 * boxes + lane);
       int page_next = in_pool(logical_next);
       int logical_far = listed(t0 * boxes + 32 + lane);
-      const int t1 = to >= base + unit ? tiles : tile_at<D, KB>(weight, tiles, static_cast<int>(to - base));
+      const int t1 = to >= base + unit ? tiles : tile_at<D, KB, NSTG>(weight, tiles, static_cast<int>(to - base));
       if (t0 < t1) {
         const int slot = t0 > 0 ? 0 : t1 < tiles ? 1 : -1;
         if (slot == 0) has_partial0 = true;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
               ok = false;
               break;
             }
-            StageInfo<D, KB>* info = &sh->info[ring.st];
+            StageInfo<D, KB, NSTG>* info = &sh->info[ring.st];
             if (tile == t) {
               info->box[lane & (boxes - 1)] = make_int2(key0, keys);
               if (lead) {
@@ -804,10 +804,10 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
   if (p.lse && e == 0) p.lse[row] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D, int KB>
+template <int D, int KB, int NSTG>
 static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  auto kern = paged_decode_kernel<D, KB>;
-  constexpr int bytes = pd_smem_bytes<D, KB>();
+  auto kern = paged_decode_kernel<D, KB, NSTG>;
+  constexpr int bytes = pd_smem_bytes<D, KB, NSTG>();
   static_assert(bytes <= 227 * 1024, "shared memory budget");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -823,9 +823,13 @@ static cudaError_t launch_pd(const PagedDecodeParams& p, const CUtensorMap& tk, 
   return launch_pdl(paged_combine_kernel<D>, dim3(kPagedCtas, p.hq / p.hkv), kCombineThreads, 0, s, p);
 }
 
+// Stages: what fits.  Over listed pages heads of 128 take one less: the memory left
+// makes the selection before it faster (48 of up to 1024 pages of 32 sequences: 44.7 us
+// together, 47.2 with five), and its pieces are short; a long cache wants five (864 us
+// against 902 for four sequences of 1048576 keys).
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  if (p.d == 128) return launch_pd<128, 1>(p, tk, tv, s);
-  return p.tile_keys == 128 ? launch_pd<64, 2>(p, tk, tv, s) : launch_pd<64, 1>(p, tk, tv, s);
+  if (p.d == 128) return p.selected ? launch_pd<128, 1, 4>(p, tk, tv, s) : launch_pd<128, 1, 5>(p, tk, tv, s);
+  return p.tile_keys == 128 ? launch_pd<64, 2, 6>(p, tk, tv, s) : launch_pd<64, 1, 8>(p, tk, tv, s);
 }
 
 }  // namespace atf
