@@ -33,7 +33,7 @@
 //
 // Measured, selection and decode of the selected pages: 64 of 16384 pages for 28 query
 // and 4 kv heads of 128, 24.5 us (15 of them here); 48 of up to 1024 pages of 32
-// sequences, 47.7 us (18 here).
+// sequences, 44.9 us (18 here).
 #include <cuda_bf16.h>
 
 #include "atf_internal.cuh"
