@@ -165,7 +165,10 @@ class Target {
     Py_DECREF(v);
     if (!s && PyErr_Occurred()) throw PythonError{};
     stream_ = static_cast<cudaStream_t>(s);
-    guard_.emplace(c10::cuda::getStreamFromExternal(stream_, dev));
+    if (stream_ == cudaStreamPerThread) throw Refusal{"stream: the per-thread default stream has no torch stream"};
+    // torch tells its own streams from handles by the low bit, which the legacy default's has set
+    guard_.emplace(stream_ == nullptr || stream_ == cudaStreamLegacy ? c10::cuda::getDefaultCUDAStream(dev)
+                                                                     : c10::cuda::getStreamFromExternal(stream_, dev));
   }
 
   template <typename Args>

@@ -310,9 +310,10 @@ def test_decode_against_oracle(lens, Hq, Hkv, d, page, theta, alpha):
     _check_decode(q, kp, vp, table, n, theta, alpha, out, lse)
 
 
-def test_decode_sharp_softmax_and_infinite_stale_slots():
+@pytest.mark.parametrize("d,page,stale", [(128, 64, math.inf), (128, 16, math.nan), (64, 128, math.nan)])
+def test_decode_sharp_softmax_and_infinite_stale_slots(d, page, stale):
     lens, theta = [900, 64, 65], 1e7
-    q, kp, vp, table, n = _decode_case(lens, 16, 2, 128, 64, theta, 1.0, stale=math.inf, std=8.0)
+    q, kp, vp, table, n = _decode_case(lens, 16, 2, d, page, theta, 1.0, stale=stale, std=8.0)
     lse = torch.empty(3, 16, device="cuda")
     out = atf.paged_decode(q, kp, vp, table, n, theta, 1.0, lse=lse)
     atf.atf_check()
@@ -630,6 +631,12 @@ def test_scratch_and_outputs_of_a_call_on_a_given_stream():
     torch.cuda.synchronize()
     atf.atf_check()
     assert all(torch.equal(o, want) and torch.equal(s, sel) for o, s in got)
+    with torch.cuda.stream(side):  # handles of the default stream, while another is current
+        got = [atf.paged_decode(*c, theta, alpha, stream=s) for s in (0, 1)]
+        with pytest.raises(TypeError, match="per-thread"):
+            atf.paged_decode(*c, theta, alpha, stream=2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got)
 
 
 def test_captured_behind_copies_and_events_of_other_streams():
