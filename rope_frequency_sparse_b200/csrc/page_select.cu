@@ -28,8 +28,8 @@
 // between the least and the greatest, and the bin of the last kept one again, until
 // few are left; a bin's edges are exact, so any distribution ends (each round parts
 // the least from the greatest).  Where the places are at most a quarter of the groups
-// of 16 pages, groups are searched by their highest scores first, and pages only in
-// those that can hold a kept one: one SM's passes over 16384 scores took 12 us.
+// of 16 pages with one that competes, those are searched by their highest scores first, and
+// pages only in those that can hold a kept one: one SM's passes over 16384 scores took 12 us.
 //
 // Measured, selection and decode of the selected pages: 64 of 16384 pages for 28 query
 // and 4 kv heads of 128, 24.5 us (15 of them here); 48 of up to 1024 pages of 32
@@ -38,6 +38,7 @@
 
 #include "atf_internal.cuh"
 #include "ptx.cuh"
+#include "select_groups.cuh"
 
 namespace atf {
 
@@ -101,7 +102,6 @@ __device__ __forceinline__ int pool_page(const PageSelectParams& p, int entry) {
 // What the first kernel leaves of a list of two pages or more in its max_pages 64-bit
 // words of workspace: the pages' scores, sortable, and of each group of 16 pages the
 // bits of the greatest S and the highest score that competes for a place (0: none).
-constexpr int kGroup = 16;
 struct Scores {
   unsigned *key, *size, *high;
   __device__ Scores(const PageSelectParams& p, int list)
@@ -488,23 +488,22 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
 
   // ---- few places in a long list: only groups whose highest score is among the
   // `places` highest of the groups, or close below, hold a kept page
-  if (groups >= 4 * places) {
+  const SelectGroups rivals = select_groups(pages, p.n_first, p.n_last, places);
+  if (rivals.search) {
     auto each_group = [&](auto f) {
 #pragma unroll 4
-      for (int i = tid; i < groups; i += T) f(i, scores.high[i], 0);
+      for (int i = rivals.first + tid; i < rivals.first + rivals.count; i += T) f(i, scores.high[i], 0);
     };
-#pragma unroll 4
-    for (int i = tid; i < groups; i += T) {
-      const unsigned k = scores.high[i];
-      if (k) lo = min(lo, k);
+    each_group([&](int i, unsigned k, int) {
+      lo = min(lo, k);
       hi = max(hi, k);
       size = max(size, scores.size[i]);
-    }
+    });
     range();
     const float slack = slack_of(size);
     if (slack < INFINITY) {
       const unsigned top = hi;
-      int need = places, count = groups;
+      int need = places, count = rivals.count;
       narrow(sh, each_group, lo, hi, need, count, kFewGroups);
       const unsigned least = below(lo, slack);
       each_group([&](int i, unsigned k, int) {
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
         for (int x0 = 0; x0 < n * kGroup; x0 += T) {
           const int x = x0 + tid, i = x < n * kGroup ? sh->groups[x / kGroup] * kGroup + x % kGroup : pages;
           const unsigned k = i < pages && !forced(i) ? scores.key[i] : 0;
-          const unsigned in = __ballot_sync(0xffffffffu, k >= least);  // least is above 0
+          const unsigned in = __ballot_sync(0xffffffffu, k >= least);  // least is above 0: `places` pages or more
           int at = 0;
           if (lane == 0) at = atomicAdd(&sh->n, __popc(in));
           at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << lane) - 1));

@@ -433,6 +433,29 @@ def test_select_against_oracle(lens, Hq, Hkv, d, page, theta, alpha, n_sel, firs
     assert np.array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("first,last,n_sel,pages,P", [
+    (1, 110, 113, range(114, 131), 0), (1, 128, 131, range(132, 165), 0), (128, 1, 131, range(132, 165), 0),
+    (1, 256, 261, range(262, 305, 3), 0), (256, 0, 260, range(261, 305, 4), 0), (1, 512, 517, range(518, 561, 6), 0),
+    (512, 3, 519, range(520, 561, 7), 0), (1, 512, 521, [560, 640, 700], 0), (600, 2, 610, [700, 760, 800], 0),
+    # the same lists in tables of other widths: other kernels, other blocks
+    (1, 128, 131, [132, 144, 150, 200], 900), (1, 256, 261, [262, 272, 300, 400], 2100),
+    (1, 900, 903, [904, 912, 960, 2100], 0), (2000, 100, 2103, [2104, 2112, 2160, 2300], 0),
+    # as many competing groups as four a place, one more and one less
+    (16, 16, 36, [32 + 16 * 15, 32 + 16 * 16, 32 + 16 * 16 + 1, 32 + 16 * 17], 0), (15, 17, 33, [32 + 49, 32 + 64, 32 + 65], 0),
+])
+def test_select_beside_long_runs_of_forced_pages(first, last, n_sel, pages, P):
+    """Few pages compete: groups of forced pages alone, and fewer competing groups than places."""
+    Hq, Hkv, d, page = 2, 1, 64, 16
+    lens = [page * n - i % page for i, n in enumerate(pages)]
+    table, pool = _tables(lens, page, 101, extra=max(0, P - max(pages)))
+    bd = torch.sort(_normal(102, pool, Hkv, 2, d), dim=2).values.contiguous()
+    q = _normal(103, len(lens), Hq, d)
+    sel = atf.page_select(q, bd, table, _int32(lens), page, n_sel, 1e4, 1.0, first, last)
+    atf.atf_check()
+    want = paged.select(paged.f64(q), paged.f64(bd), table.cpu().numpy(), lens, page, n_sel, 1e4, 1.0, first, last)
+    assert np.array_equal(sel.cpu().numpy(), want)
+
+
 def test_select_ties_go_to_the_lowest_index():
     """Every page of a sequence the same (or two kinds of pages): equal scores."""
     Hkv, d, page, n = 2, 64, 16, 16 * 3000
