@@ -246,7 +246,8 @@ struct SelectShared {
 
 // Narrows [lo, hi], which holds the need-th highest of the keys that each(f) calls
 // f(i, key, j) for, until it is one key, or all of its `count` keys are needed, or they
-// are at most `few`.  On return `need` counts within [lo, hi].
+// are at most `few`.  On return `need` counts within [lo, hi].  Each round takes kBinBits
+// off the range; a rank that the keys do not hold ends the search where it stands.
 template <typename K, typename Each>
 __device__ __forceinline__ void narrow(SelectShared* sh, Each each, K& lo, K& hi, int& need, int& count, int few) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
@@ -254,6 +255,7 @@ __device__ __forceinline__ void narrow(SelectShared* sh, Each each, K& lo, K& hi
     const int shift = max(0, static_cast<int>(sizeof(K)) * 8 - leading_zeros(hi - lo) - kBinBits);
     for (int i = tid; i < kBins; i += T) sh->hist[i] = 0;
     __syncthreads();
+    if (tid == 0) sh->lo = sh->hi = lo, sh->need = need, sh->count = count;  // what a bin with the rank replaces
     each([&](int, K k, int) {
       if (k >= lo && k <= hi) atomicAdd(&sh->hist[static_cast<int>((k - lo) >> shift)], 1);
     });

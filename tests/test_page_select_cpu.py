@@ -95,8 +95,12 @@ def rule(tmp_path_factory):
     return call
 
 
-def _narrow(keys, lo, hi, need, count, few, bits=32):
-    """[lo, hi] narrowed to the bin of the need-th highest key, round by round."""
+# what a round leaves where no bin holds the rank: the state that one thread sets beforehand
+PRESET = re.search(r"if \(tid == 0\) sh->lo = sh->hi = lo, sh->need = need, sh->count = count;", SOURCE) is not None
+
+
+def _narrow(keys, lo, hi, need, count, few, bits=32, held=True):
+    """[lo, hi] narrowed to the bin of the need-th highest key, round by round; held: the keys hold that rank."""
     rounds = 0
     while lo < hi and count > few and count != need:
         shift = max(0, (hi - lo).bit_length() - BIN_BITS)
@@ -110,7 +114,11 @@ def _narrow(keys, lo, hi, need, count, few, bits=32):
                 found = b
                 break
             before += hist[b]
-        assert found is not None, "a rank that no bin holds"
+        assert found is not None or not held, "a rank that no bin holds"
+        if found is None:
+            assert PRESET, "a round that reads what nobody wrote"
+            hi = lo
+            continue
         lo = lo + (found << shift)
         hi = min(hi, lo + (1 << shift) - 1)
         need, count = need - before, hist[found]
@@ -169,3 +177,15 @@ def test_search_over_groups_is_a_sort(rule, seed):
         want = sorted(range(first, pages - last), key=lambda i: (-score[i], i))[:places]
         assert got == sorted(want), (pages, first, last, n)
     assert searched
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_narrowing_ends_whatever_it_is_given(seed):
+    """Ranks that the keys do not hold, counts that are not theirs, keys outside the range."""
+    r = random.Random(seed)
+    for _ in range(20):
+        bits = r.choice([32, 64])
+        keys = [r.randrange(1 << r.randint(1, bits)) for _ in range(r.choice([0, 1, 5, 300]))]
+        lo, hi = sorted(r.randrange(1 << r.randint(1, bits)) for _ in range(2))
+        _narrow(keys, lo, hi, r.randint(0, 2 * len(keys) + 2), r.randint(0, 2 * len(keys) + 2), r.choice([1, 24]), bits,
+                held=False)
