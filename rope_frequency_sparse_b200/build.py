@@ -6,6 +6,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -57,7 +58,7 @@ def _build_tensor_calls(force):
         return
 
     home = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or NVCC)))  # NVCC may be a bare name
     inc = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
            os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
     tmp = TENSOR_CALLS + f".tmp{os.getpid()}"

@@ -41,3 +41,21 @@ def test_the_library_is_linked_where_its_torch_module_fails(fake):
     with pytest.raises(RuntimeError, match="Python.h"):
         build.build()
     assert os.path.exists(build.LIB)
+
+
+@pytest.mark.parametrize("how", ["path", "name", "link"])
+def test_cuda_headers_are_found_however_nvcc_is_named(fake, monkeypatch, tmp_path, how):
+    home = tmp_path / "cuda"
+    for f in (home / "bin" / "nvcc", home / "include" / "cuda_runtime_api.h"):
+        f.parent.mkdir(parents=True)
+        f.write_text("#!/bin/sh\n")
+    nvcc = home / "bin" / "nvcc"
+    nvcc.chmod(0o755)
+    if how == "link":
+        (tmp_path / "elsewhere").mkdir()
+        (tmp_path / "elsewhere" / "nvcc").symlink_to(nvcc)
+    monkeypatch.setenv("PATH", str(home / "bin") + os.pathsep + os.environ["PATH"])
+    monkeypatch.setattr(build, "NVCC", {"path": str(nvcc), "name": "nvcc", "link": str(tmp_path / "elsewhere" / "nvcc")}[how])
+    build.build()
+    (gxx,) = [c for c in fake[0] if c[0] == "g++"]
+    assert str((home / "include").resolve()) in [os.path.realpath(a[2:]) for a in gxx if a.startswith("-I")]
