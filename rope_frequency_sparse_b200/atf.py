@@ -438,8 +438,10 @@ def _tensor_calls():
 
         import torch  # noqa: F401  the module links to its libraries
 
+        from .build import tensor_calls_path
+
         lib = load_library()
-        path = os.path.join(_HERE, "_tensor_calls.so")
+        path = tensor_calls_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is not built; run __graft_entry__.build() "
                                "(or python -m rope_frequency_sparse_b200.build)")

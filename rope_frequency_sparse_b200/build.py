@@ -1,6 +1,7 @@
 """Build step for the CUDA library: compiles csrc/*.cu for sm_100a with nvcc and
 links libatf.so next to this file (in-tree, so it ships with the package), and
-csrc/tensor_calls.cpp, its calls on torch tensors, to _tensor_calls.so."""
+csrc/tensor_calls.cpp, its calls on torch tensors, to a module named after the
+torch and Python that it was built against."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -16,7 +17,6 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatf.so")
-TENSOR_CALLS = os.path.join(HERE, "_tensor_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -47,27 +47,37 @@ def _compile(src, verbose):
     return obj
 
 
+def tensor_calls_path() -> str:
+    """The module for this torch and this Python, whose C++ and C interfaces it is compiled against: after an
+    upgrade of either it is another file, to be built anew."""
+    import torch
+
+    return os.path.join(HERE, f"_tensor_calls-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _build_tensor_calls(force):
     src = os.path.join(SRC, "tensor_calls.cpp")
-    if not force and not _stale(TENSOR_CALLS, [src, os.path.join(ROOT, "include", "atf.h")]):
-        return
     try:
         import torch
+
+        target = tensor_calls_path()
     except ImportError:
-        print("torch is not installed: _tensor_calls.so is left out, the C library is complete", file=sys.stderr)
+        print("torch is not installed: its module is left out, the C library is complete", file=sys.stderr)
+        return
+    if not force and not _stale(target, [src, os.path.join(ROOT, "include", "atf.h")]):
         return
 
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or NVCC)))  # NVCC may be a bare name
     inc = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
            os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    tmp = TENSOR_CALLS + f".tmp{os.getpid()}"
+    tmp = target + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + d for d in inc), src, "-o", tmp,
            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TENSOR_CALLS)
+    os.replace(tmp, target)
 
 
 def build(verbose: bool = False, force: bool = False) -> str:

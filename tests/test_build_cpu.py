@@ -3,10 +3,11 @@ here, the commands and the files that they leave are looked at."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
-from rope_frequency_sparse_b200 import build
+from rope_frequency_sparse_b200 import atf, build
 
 
 @pytest.fixture
@@ -14,7 +15,7 @@ def fake(monkeypatch, tmp_path):
     """A build into an empty folder whose compilers write their output file and do nothing else."""
     monkeypatch.setattr(build, "BUILD", str(tmp_path / "objects"))
     monkeypatch.setattr(build, "LIB", str(tmp_path / "libatf.so"))
-    monkeypatch.setattr(build, "TENSOR_CALLS", str(tmp_path / "_tensor_calls.so"))
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
     commands = []
 
     def run(cmd, **kw):
@@ -30,10 +31,14 @@ def fake(monkeypatch, tmp_path):
     return commands, fake_gxx
 
 
+def _modules():
+    return sorted(f for f in os.listdir(build.HERE) if f.startswith("_tensor_calls"))
+
+
 def test_the_library_is_built_without_torch(fake, monkeypatch, capsys):
     monkeypatch.setitem(sys.modules, "torch", None)
     assert build.build() == build.LIB and os.path.exists(build.LIB)
-    assert not os.path.exists(build.TENSOR_CALLS) and "torch" in capsys.readouterr().err
+    assert not _modules() and "torch" in capsys.readouterr().err
 
 
 def test_the_library_is_linked_where_its_torch_module_fails(fake):
@@ -59,3 +64,28 @@ def test_cuda_headers_are_found_however_nvcc_is_named(fake, monkeypatch, tmp_pat
     build.build()
     (gxx,) = [c for c in fake[0] if c[0] == "g++"]
     assert str((home / "include").resolve()) in [os.path.realpath(a[2:]) for a in gxx if a.startswith("-I")]
+
+
+def test_another_torch_or_python_gets_a_module_of_its_own(fake, monkeypatch):
+    import torch
+
+    build.build()
+    build.build()
+    assert len(_modules()) == 1 and len([c for c in fake[0] if c[0] == "g++"]) == 1
+    monkeypatch.setattr(torch, "__version__", "99.1.2")
+    build.build()
+    assert len(_modules()) == 2 and any("99.1.2" in f for f in _modules())
+    suffix = sysconfig.get_config_var
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else suffix(n))
+    build.build()
+    assert len(_modules()) == 3
+
+
+def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
+    import torch
+
+    build.build()
+    monkeypatch.setattr(atf, "_calls", None)
+    monkeypatch.setattr(torch, "__version__", "99.1.2")
+    with pytest.raises(RuntimeError, match="99.1.2.*is not built"):
+        atf._tensor_calls()
