@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
           const int tg1 = min(t1, tg + (32 >> (C::TILE_LOG2 - box_log2)));
           for (int t = tg; t < tg1; ++t, ++it, ring.next()) {
             if (it % kPdProducers != pw) continue;
-            if (it >= NSTG && !warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x501)) {
+            if (it >= NSTG && !warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x601)) {
               ok = false;
               break;
             }
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
       more = b < p.batch && base < to;
     }
     if (ok && it % kPdProducers == pw) {  // the end mark
-      if (it >= NSTG) ok = warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x502);
+      if (it >= NSTG) ok = warp_wait(&sh->empty[ring.st], ring.parity ^ 1, &sh->abort, p.err, 0x602);
       if (ok && lane == 0) {
         sh->info[ring.st].tile.y = kEnd;
         mbar_arrive(&sh->full[ring.st]);
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
           seen = now;
           t0 = clock64();
         } else if (clock64() - t0 > kWaitLimitCycles) {
-          atomicCAS(p.err, 0u, 0x504u);
+          atomicCAS(p.err, 0u, 0x604u);
           sh->abort = 1;
         }
       }
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   int pieces = 0, passed = 0;
   RingPos<NSTG> ring;
   // the joiners are done with the last piece's states (a bounded wait)
-  auto joined = [&] { return pieces == 0 || warp_wait(&sh->joined, (pieces - 1) & 1, &sh->abort, p.err, 0x505); };
+  auto joined = [&] { return pieces == 0 || warp_wait(&sh->joined, (pieces - 1) & 1, &sh->abort, p.err, 0x605); };
   auto leave = [&](int b, int hk, int slot) {
     if (tid == 0) sh->left_b = b, sh->left_hk = hk, sh->left_slot = slot;
     __syncwarp();
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kPdThreads, 1)
   };
   for (int turn = 0;; turn = turn + 1 == kPdGroups ? 0 : turn + 1) {
     const int st = ring.st;
-    if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x503)) return;
+    if (!warp_wait(&sh->full[st], ring.parity, &sh->abort, p.err, 0x603)) return;
     ring.next();
     const int4 tile = sh->info[st].tile;
     int2 my[KB];
