@@ -5,8 +5,8 @@ Tolerances.  A rounding to bf16 is off by at most 2^-8 of the value, to fp32 by 
 Norm and rotation run in fp32: the sum of d <= 128 squares is off by at most 2^-17
 relative, half of that after the square root, the other steps by a few 2^-24, the sine
 and cosine of a turn's fraction by 2^-22 (for bf16 rows by 2^-21): together below 2^-16 of |a| + |b| of the
-pair.  The decode rounds each softmax weight to bf16 (2^-8 of the weighted |v|); a
-logit is off by at most 18 * 2^-23 a tensor-core step of the sum of |q k| (the bound
+pair.  The decode's softmax weights are allowed a rounding to bf16 (2^-8 of the weighted
+|v|; test_decode_weights_keep_their_low_bits holds them to 2^-16); a logit is off by at most 18 * 2^-23 a tensor-core step of the sum of |q k| (the bound
 the FASA scores are held to), which scales a weight by as much, twice (numerator and
 sum); exponentials and sums add less than 2^-16.
 """
@@ -340,6 +340,34 @@ def test_decode_over_listed_pages(lens, Hq, Hkv, d, page, n_sel):
     out = atf.paged_decode(q, kp, vp, table, n, theta, alpha, selected=sel, lse=lse)
     atf.atf_check()
     _check_decode(q, kp, vp, table, n, theta, alpha, out, lse, sel)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page,extra,listed", [
+    ([2, 3, 17, 40, 130] * 4, 28, 4, 128, 16, 0, False), ([2, 3, 17, 40, 130] * 4, 8, 1, 128, 64, 0, True),
+    ([2, 3, 17, 40, 130] * 4, 6, 2, 64, 16, 0, False), ([5, 33, 129, 300] * 5, 16, 2, 64, 32, 80, False),
+    ([5, 33, 129, 300] * 5, 16, 2, 64, 128, 20, True)])
+def test_decode_weights_keep_their_low_bits(lens, Hq, Hkv, d, page, extra, listed):
+    """Few keys of both signs: what a weight loses shows where the values nearly cancel.  A weight in two bf16
+    parts is off by 2^-8 of 2^-8; the products with the values, two a block of 16 keys and a warp, add 18 * 2^-23
+    of the sum so far each (a warp takes one block of 128 keys).  A table of that width takes the tiles of 128
+    keys for heads of 64."""
+    theta, alpha = 1e4, 1.0
+    q, kp, vp, table, n = _decode_case(lens, Hq, Hkv, d, page, theta, alpha, seed=67)
+    if extra:
+        table = torch.cat([table, torch.full((len(lens), extra), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+        assert table.shape[1] * page * len(lens) * Hkv >= 8 * 64 * 148 or listed
+    sel = None
+    if listed:
+        P = -(-max(lens) // page)
+        sel = torch.arange(P, dtype=torch.int32, device="cuda").expand(len(lens), Hkv, P).contiguous()
+    lse = torch.empty(len(lens), Hq, device="cuda")
+    out = atf.paged_decode(q, kp, vp, table, n, theta, alpha, selected=sel, lse=lse)
+    atf.atf_check()
+    want, _, weight, spread = paged.decode(paged.f64(q), paged.f64(kp), paged.f64(vp), table.cpu().numpy(), lens, theta,
+                                           alpha, None if sel is None else sel.cpu().numpy())
+    step = 18 * 2.0 ** -23 * (d // 16) * spread + 2.0 ** -16
+    summed = 18 * 2.0 ** -23 * 2 * (max(lens) // 128 + 1)
+    _within(out, want, (2.0 ** -16 + summed + 2 * step[..., None]) * weight + 2.0 ** -8 * np.abs(want))
 
 
 def test_decode_of_every_page_listed_is_the_plain_decode():
