@@ -304,7 +304,8 @@ size_t atf_fasa_workspace_bytes(int batch, int heads, long long n_cache, int bud
  * same pass: what sits between a fused projection and the attention.
  *   y = x / sqrt(mean(x^2) + eps) * weight  over the d elements of a head (a NULL
  *       weight: y = x), then pair i of y is turned by pos[axis of i] * theta^(-2i/d).
- * Computed in fp32 (angles reduced exactly) and rounded once.  The outputs hold
+ * Computed in fp32 and rounded once; an angle is reduced to a fraction of a turn that is
+ * off by 2^-26 of a turn at most, at any position.  The outputs hold
  * pair i in dims (2i, 2i+1): what atf_prefill_ex reads with rotated = 1. */
 typedef struct {
   const void *q, *k;       /* token t, head h at element t * stride + h * d of [tokens][...]; slices of one
@@ -371,7 +372,9 @@ typedef struct {
 atf_status atf_paged_append(const atf_paged_append_args* args, void* stream);
 
 /* Decode over a paged cache: one query per sequence, at position kv_len[b] - 1, with the
- * windows of the method, over every key of the sequence or over the pages of a list. */
+ * windows of the method, over every key of the sequence or over the pages of a list.  Logits,
+ * softmax statistics and the output's sum are fp32; a softmax weight enters its product with
+ * the values as two bf16 parts, off by 2^-16 of it. */
 typedef struct {
   const void* q;           /* bf16 [batch] rows of [heads][d], ALREADY rotated (atf_paged_append's q_out) */
   long long q_stride;      /* elements from a sequence to the next: >= heads * d, rows 16-byte aligned */

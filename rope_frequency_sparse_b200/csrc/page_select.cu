@@ -32,7 +32,7 @@
 // pages only in those that can hold a kept one: one SM's passes over 16384 scores took 12 us.
 //
 // Measured, selection and decode of the selected pages: 64 of 16384 pages for 28 query
-// and 4 kv heads of 128, 24.5 us (15 of them here); 48 of up to 1024 pages of 32
+// and 4 kv heads of 128, 24.3 us (15 of them here); 48 of up to 1024 pages of 32
 // sequences, 44.9 us (18 here).
 #include <cuda_bf16.h>
 

@@ -20,10 +20,11 @@
 // at most two pieces (the first and the last of its list), each written as a partial
 // (sum, max, row sum), and a second kernel joins them.
 //
-// Measured, 28 query and 4 kv heads of 128, theta 1e7, alpha 1: 873 us for four
-// sequences of 1048576 keys (98 % of the copy rate on the bytes needed), 82 us for 64
-// of up to 8192 in pages of 16 (85 %), 39.5 us for one of 131072 (75 %: about 4 us
-// until the first tile and 3 from the last to the joined output).
+// Measured, 28 query and 4 kv heads of 128, theta 1e7, alpha 1, a few passes from a cool
+// start: 887 us for four sequences of 1048576 keys (97 % of the copy rate on the bytes
+// needed), 82.7 us for 64 of up to 8192 in pages of 16 (85 %), 39.6 us for one of 131072
+// (74 %: about 4 us until the first tile and 3 from the last to the joined output).  Call
+// after call the largest runs into the power limit: 1010 to 1045 us (82 to 85 %).
 //
 // Inside a CTA four producer warps walk the list and fill a ring of tiles with TMA,
 // every fourth tile each; a lane looks up the page of one box of 32, a group of
@@ -37,9 +38,9 @@
 // goes from accumulators to operand by a register transpose (movmatrix).  P goes into
 // the product with V as two bf16 parts, a weight and what its rounding left, off by
 // 2^-16 of the weight: the output is then off by its own rounding alone (rms against 64
-// bits 0.0017; 0.0024 with P in one part, at 131072 keys).  The second product costs 16 us of 887 for four
-// sequences of 1048576 keys and 0.3 of 82.6 for the batch of 64.  The weights' sums, the maxima and
-// O stay fp32.
+// bits 0.0017; 0.0024 with P in one part, at 131072 keys).  The second product costs 14 us of
+// 887 for four sequences of 1048576 keys (58 of 1043 at the power limit) and 0.4 of 82.7 for
+// the batch of 64.  The weights' sums, the maxima and O stay fp32.
 #include <cuda_bf16.h>
 
 #include <atomic>
