@@ -305,7 +305,7 @@ size_t atf_fasa_workspace_bytes(int batch, int heads, long long n_cache, int bud
  *   y = x / sqrt(mean(x^2) + eps) * weight  over the d elements of a head (a NULL
  *       weight: y = x), then pair i of y is turned by pos[axis of i] * theta^(-2i/d).
  * Computed in fp32 and rounded once; an angle is reduced to a fraction of a turn that is
- * off by 2^-26 of a turn at most, at any position.  The outputs hold
+ * off by less than 2^-25 of a turn, at any position.  The outputs hold
  * pair i in dims (2i, 2i+1): what atf_prefill_ex reads with rotated = 1. */
 typedef struct {
   const void *q, *k;       /* token t, head h at element t * stride + h * d of [tokens][...]; slices of one

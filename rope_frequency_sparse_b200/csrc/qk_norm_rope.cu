@@ -9,7 +9,7 @@
 // 64-bit integer product that wraps (at position 2^20 an fp32 angle is off by more
 // than a bf16 step; the product's table entry by 2^-34 turns at 2^31, and it takes a third
 // of the time of fp64's multiply, round and convert).  Its upper 32 bits become an fp32
-// number, half a step of which is 2^-26 of a turn: the angle's error at any position.  The sine
+// number, half a step of which is 2^-26 of a turn: all but 2^-31 of the angle's error, at any position.  The sine
 // and cosine of that fraction are fp32's for fp32 rows; for bf16 rows the fast ones,
 // off by at most 2^-21 on [-pi, pi], 2^-13 of a bf16 half step.
 //
